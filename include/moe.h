@@ -406,6 +406,158 @@ MOE_API int64_t moe_ep_plan(const int32_t* counts, int G, int E, int rank, int32
                             int32_t* recv_counts, int32_t* local_offsets);
 
 /*
+ * Router training: the balance loss of a routed batch, the gradient of the
+ * combine and the gradient of the router's logits.  They take the buffers
+ * that moe_route, moe_permute and moe_grouped_ffn wrote in the forward pass.
+ * SwiGLU kind only (else MOE_ERR_UNSUPPORTED).  E = n_ffn + n_zero + n_copy +
+ * n_const router rows; every sum is fp32 or wider and is formed in an order
+ * that depends on the sizes only, so equal inputs give equal bits.  (The
+ * pages name balanced expert load as a training concern and give no formula;
+ * these are the usual ones.)
+ */
+
+/*
+ * Balance loss, router z-loss and per-expert counts.
+ *   counts[e] = slots of counted tokens that chose expert e; counts[E] = n, the
+ *   counted tokens; p_t = softmax(logits_t) over the E rows;
+ *   prob_mean[e] = (1/n) sum_t p_te;
+ *   losses[0] = E sum_e weight_e (counts[e] / (n top_k)) prob_mean[e];
+ *   losses[1] = (1/n) sum_t logsumexp(logits_t)^2.
+ * A token is counted if token_mask is NULL or its byte is nonzero (padding
+ * rows of a batch carry 0).  With no counted token all outputs are 0.  A
+ * row whose logits are all -inf has p = 0 and adds nothing to either loss.
+ * logits [T, E] fp32 as moe_route writes them; topk_idx [T, top_k];
+ * token_mask [T] bytes, nullable; expert_weight [E] fp32, nullable (all 1:
+ * a MoE++ layer may weigh its zero-computation experts less); counts [E + 1]
+ * int32; prob_mean [E] fp32; losses [2] fp32.  An id outside [0, E) sets
+ * MOE_ERR_DEVICE_BOUNDS and is not counted.  workspace: at least
+ * moe_balance_loss_workspace_size(desc) bytes (-1: invalid descriptor or
+ * another kind), its contents need no clearing; calls that may overlap must
+ * not share it.
+ */
+MOE_API int64_t moe_balance_loss_workspace_size(const moe_layer_desc* desc);
+MOE_API moe_status moe_balance_loss(const moe_layer_desc* desc, const float* logits, const int32_t* topk_idx,
+                                    const uint8_t* token_mask, const float* expert_weight, int32_t* counts,
+                                    float* prob_mean, float* losses, void* workspace, size_t ws_bytes,
+                                    moe_stream_t stream);
+
+/*
+ * Gradient of the router's logits, from the two losses of moe_balance_loss and
+ * from the gates, in one pass over the logits:
+ *   dlogits[t, e] = [t counted] (p_te / n) (dlosses[0] E (wf_e - sum_i p_ti wf_i)
+ *                                           + 2 dlosses[1] logsumexp(logits_t))
+ *                 + sum over j with topk_idx[t, j] = e of
+ *                   g_tj (dgate_tj - sum_i g_ti dgate_ti),
+ *   wf_e = weight_e counts[e] / (n top_k), g = topk_gate.
+ * The counts are constants of the batch, as usual for this loss: its gradient
+ * goes through the probabilities.  counts [E + 1] as moe_balance_loss writes
+ * them (a data-parallel caller may have summed them over its ranks);
+ * dlosses [2] fp32 on the device: the upstream gradients of the two losses;
+ * NULL leaves the loss terms out (token_mask, expert_weight and counts are
+ * then not read).  dgate [T, top_k] fp32; NULL leaves the gate term out
+ * (topk_idx and topk_gate are then not read).  The token mask concerns the
+ * loss terms only.  dlogits [T, E] fp32 is also the gradient of prev_logits;
+ * its column sums are the gradient of router_bias (moe_linear_backward's db).
+ * dlogits may be `logits` itself.
+ */
+MOE_API moe_status moe_route_backward(const moe_layer_desc* desc, const float* logits, const int32_t* topk_idx,
+                                      const float* topk_gate, const float* dgate, const uint8_t* token_mask,
+                                      const float* expert_weight, const int32_t* counts, const float* dlosses,
+                                      float* dlogits, moe_stream_t stream);
+
+/*
+ * Gradient of moe_combine, from dy [T, d_model] (y's type: dtype, or fp32 if
+ * desc->out_f32).  With O_j the output of slot j's expert as in moe_combine:
+ *   dgate[t, j] = <dy_t, O_j>                                (fp32 [T, top_k]);
+ *   dy_sorted[row_of[t, j]] = topk_gate[t, j] dy_t for FFN experts, and
+ *     dy_sorted[off[n_ffn + s] + t] = dy_t for shared expert s
+ *     (dtype [row capacity, d_model]; other rows are untouched);
+ *   dx[t] = (sum of g over copy slots + sum of g a1 over constant slots) dy_t
+ *     (dtype [T, d_model]: the zero-computation terms alone);
+ *   dconst_mix[t, c] = (sum of g) (<dy_t, x_t>, <dy_t, v_c>) over the slots of
+ *     constant expert c (fp32 [T, n_const, 2]);
+ *   dconst_vec[c] = sum over those slots of g a2 dy_t  (fp32 [n_const, d_model]).
+ * Each output is nullable; those that are NULL are not computed, and what only
+ * they need may be NULL too: y_sorted (dgate), x (dgate, dconst_mix; layers
+ * with copy or constant experts), const_mix and w->const_vec (constant
+ * experts; dgate, dx, dconst_mix, dconst_vec), expert_offsets (dy_sorted of
+ * shared experts), row_of (layers with FFN experts).  An id or row out of
+ * range sets MOE_ERR_DEVICE_BOUNDS and its slot counts as a zero expert's.
+ */
+MOE_API moe_status moe_combine_backward(const moe_layer_desc* desc, const moe_layer_weights* w, const void* dy,
+                                        const void* y_sorted, const int32_t* expert_offsets,
+                                        const int32_t* row_of, const int32_t* topk_idx, const float* topk_gate,
+                                        const float* const_mix, const void* x, float* dgate, void* dy_sorted,
+                                        void* dx, float* dconst_mix, float* dconst_vec, moe_stream_t stream);
+
+/*
+ * Dense product with bias, activation and residual, and its gradients: the
+ * projections that stand beside the routed experts, and the router's own
+ * product z = W_r x + b + z_prev where it is trained.
+ *   z = x W^T + bias,  y = act(z) + residual.
+ * Types: x, w `dtype`; bias fp32; y and residual `dtype`, or fp32 if out_f32;
+ * the pre-activation z (kept for the backward pass) `dtype`.  Products are
+ * accumulated in fp32 (bf16 on tcgen05 tensor cores, fp32 on FMA pipes) and
+ * each result is rounded once.
+ */
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,          /* max(z, 0), slope 0 at z <= 0        */
+    MOE_ACT_SILU = 2,          /* z / (1 + exp(-z))                   */
+    MOE_ACT_GELU = 3           /* z Phi(z), exact (erf)               */
+} moe_act;
+
+/* Sizes of one dense product.  Row strides (ld_*) are in elements, at least
+ * the row's length; 0 stands for the row's length. */
+typedef struct moe_linear_desc {
+    int32_t M;                 /* rows of x and y (tokens), >= 0                     */
+    int32_t N;                 /* columns of y: rows of w, >= 1                      */
+    int32_t K;                 /* columns of x and w, >= 1                           */
+    int32_t dtype;             /* moe_dtype of x, w, z, dx and (see grad_f32) dw     */
+    int32_t act;               /* moe_act                                            */
+    int32_t out_f32;           /* 1: y, residual and dy are fp32                     */
+    int32_t grad_f32;          /* 1: dw is fp32, and dz enters its product with 24   *
+                                * significant bits; 0: dw is dtype                   */
+    int32_t ld_x;              /* x [M, K]                                           */
+    int32_t ld_w;              /* w [N, K]                                           */
+    int32_t ld_y;              /* y (forward) or dy (backward) [M, N]                */
+    int32_t ld_r;              /* residual [M, N]                                    */
+    int32_t ld_z;              /* z [M, N]                                           */
+    int32_t ld_dx;             /* dx [M, K]                                          */
+} moe_linear_desc;
+
+/* Scratch bytes of moe_linear and moe_linear_backward (0: none needed, the
+ * workspace may be NULL); -1 for an invalid descriptor. */
+MOE_API int64_t moe_linear_workspace_size(const moe_linear_desc* desc);
+MOE_API int64_t moe_linear_backward_workspace_size(const moe_linear_desc* desc);
+
+/*
+ * bias [N], residual [M, N] and z [M, N] are nullable; y may be `residual`
+ * itself (then ld_y = ld_r); no other output may overlap an input.  Tensor
+ * bases 16-byte aligned.  Rows whose stride is not a multiple of 16 bytes are
+ * first copied into the workspace (bf16).  Calls that may overlap must not
+ * share a workspace.
+ */
+MOE_API moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
+                              const void* residual, void* y, void* z, void* workspace, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/*
+ * Gradients from dy [M, N] (y's type):
+ *   dz = dy act'(z);  dx = dz W [M, K] (dtype);  dw = dz^T x [N, K] (dtype, or
+ *   fp32 if grad_f32; contiguous);  db = sum over rows of dz [N] (fp32).
+ * The residual's gradient is dy itself.  z: as moe_linear wrote it (required
+ * unless act is MOE_ACT_NONE).  Each output is nullable; x is needed for dw
+ * only, w for dx only.  bf16: dz is rounded to bf16 once before the products
+ * (exact when act is MOE_ACT_NONE and dy is bf16); with grad_f32, dw takes it
+ * in three bf16 parts instead.  db sums the unrounded dz.  M = 0 gives dw = 0
+ * and db = 0.
+ */
+MOE_API moe_status moe_linear_backward(const moe_linear_desc* desc, const void* x, const void* w, const void* z,
+                                       const void* dy, void* dx, void* dw, float* db, void* workspace,
+                                       size_t ws_bytes, moe_stream_t stream);
+
+/*
  * Self-test of the kernels' bounded waits (no counterpart on the pages): a
  * one-thread kernel waits on an mbarrier that nothing arrives on, giving up
  * after limit_ns nanoseconds (0 < limit_ns <= 2e9) the way every wait in the

@@ -19,13 +19,16 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_DEVICE_BOUNDS, MOE_ERR_TIMEOUT = 4, 5, 6
 MOE_F32, MOE_BF16 = 0, 1
 MOE_EXPERT_SWIGLU, MOE_EXPERT_ATOMIC_GELU = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU = 0, 1, 2, 3
 
 EXPORTED = ("moe_num_groups", "moe_row_capacity", "moe_workspace_size", "moe_layer_workspace_size",
             "moe_route", "moe_permute", "moe_grouped_ffn", "moe_grouped_ffn_phase", "moe_combine",
             "moe_layer_forward", "moe_get_device_status", "moe_status_string",
             "moe_last_launch_count", "moe_permute_static", "moe_selftest_wait_timeout",
             "moe_layer_host_workspace_size", "moe_layer_forward_host", "moe_ep_expert_range", "moe_ep_owner",
-            "moe_ep_plan", "moe_fused_workspace_size", "moe_fused_ffn_combine")
+            "moe_ep_plan", "moe_fused_workspace_size", "moe_fused_ffn_combine",
+            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward", "moe_combine_backward",
+            "moe_linear_workspace_size", "moe_linear_backward_workspace_size", "moe_linear", "moe_linear_backward")
 
 
 class MoEError(RuntimeError):
@@ -45,6 +48,11 @@ class MoELayerWeights(ctypes.Structure):
         "w_router", "router_bias", "w_const_mix", "const_vec", "w_gate", "w_up", "w_down",
         "ws_gate", "ws_up", "ws_down", "w_query", "subkeys_row", "subkeys_col", "u", "v",
         "s_gate", "s_up", "s_down", "ss_gate", "ss_up", "ss_down")]
+
+
+class MoELinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "M", "N", "K", "dtype", "act", "out_f32", "grad_f32", "ld_x", "ld_w", "ld_y", "ld_r", "ld_z", "ld_dx")]
 
 
 _lib = None
@@ -89,9 +97,21 @@ def load(path: Path | str | None = None):
     L.moe_ep_owner.restype = I32
     L.moe_ep_plan.argtypes = [VP, ctypes.c_int, ctypes.c_int, ctypes.c_int, VP, VP, VP]
     L.moe_ep_plan.restype = I64
+    LD = P(MoELinearDesc)
+    L.moe_balance_loss_workspace_size.argtypes = [D]
+    L.moe_linear_workspace_size.argtypes = [LD]
+    L.moe_linear_backward_workspace_size.argtypes = [LD]
+    for name in ("moe_balance_loss_workspace_size", "moe_linear_workspace_size", "moe_linear_backward_workspace_size"):
+        getattr(L, name).restype = I64
+    L.moe_balance_loss.argtypes = [D, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
+    L.moe_route_backward.argtypes = [D, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP]
+    L.moe_combine_backward.argtypes = [D, W, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP]
+    L.moe_linear.argtypes = [LD, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
+    L.moe_linear_backward.argtypes = [LD, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
     for name in ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_grouped_ffn_phase", "moe_combine",
                  "moe_layer_forward", "moe_get_device_status", "moe_permute_static", "moe_fused_ffn_combine",
-                 "moe_selftest_wait_timeout", "moe_layer_forward_host"):
+                 "moe_selftest_wait_timeout", "moe_layer_forward_host", "moe_balance_loss", "moe_route_backward",
+                 "moe_combine_backward", "moe_linear", "moe_linear_backward"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -237,6 +257,71 @@ def moe_fused_ffn_combine(desc, weights, phase, x, x_sorted, topk_idx, topk_gate
                                         _p(topk_idx),
                                         _p(topk_gate), _p(const_mix), _p(expert_offsets), _p(row_of), _p(token_of),
                                         _p(y), _p(workspace), _nbytes(workspace), _stream(stream)))
+
+
+# ------------------------------------------------------------ training
+
+def moe_balance_loss_workspace_size(desc: MoELayerDesc) -> int:
+    return int(load().moe_balance_loss_workspace_size(ctypes.byref(desc)))
+
+
+def moe_balance_loss(desc, logits, topk_idx, token_mask, expert_weight, counts, prob_mean, losses, workspace,
+                     stream=None) -> None:
+    """token_mask (uint8 or bool) and expert_weight may be None."""
+    _check("moe_balance_loss",
+           load().moe_balance_loss(ctypes.byref(desc), _p(logits), _p(topk_idx), _p(token_mask), _p(expert_weight),
+                                   _p(counts), _p(prob_mean), _p(losses), _p(workspace), _nbytes(workspace),
+                                   _stream(stream)))
+
+
+def moe_route_backward(desc, logits, topk_idx, topk_gate, dgate, token_mask, expert_weight, counts, dlosses, dlogits,
+                       stream=None) -> None:
+    """dgate None leaves the gates' term out, dlosses None the two losses'."""
+    _check("moe_route_backward",
+           load().moe_route_backward(ctypes.byref(desc), _p(logits), _p(topk_idx), _p(topk_gate), _p(dgate),
+                                     _p(token_mask), _p(expert_weight), _p(counts), _p(dlosses), _p(dlogits),
+                                     _stream(stream)))
+
+
+def moe_combine_backward(desc, weights, dy, y_sorted, expert_offsets, row_of, topk_idx, topk_gate, const_mix, x, dgate,
+                         dy_sorted, dx, dconst_mix, dconst_vec, stream=None) -> None:
+    """Each of the five outputs may be None."""
+    ws = weights if isinstance(weights, MoELayerWeights) else weights_struct(weights)
+    _check("moe_combine_backward",
+           load().moe_combine_backward(ctypes.byref(desc), ctypes.byref(ws), _p(dy), _p(y_sorted), _p(expert_offsets),
+                                       _p(row_of), _p(topk_idx), _p(topk_gate), _p(const_mix), _p(x), _p(dgate),
+                                       _p(dy_sorted), _p(dx), _p(dconst_mix), _p(dconst_vec), _stream(stream)))
+
+
+def _rp(t):
+    """Device pointer of a 2-D tensor whose rows may lie apart (the descriptor holds the stride)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("libmoe takes 2-D tensors with contiguous rows")
+    return t.data_ptr()
+
+
+def moe_linear_workspace_size(desc: MoELinearDesc) -> int:
+    return int(load().moe_linear_workspace_size(ctypes.byref(desc)))
+
+
+def moe_linear_backward_workspace_size(desc: MoELinearDesc) -> int:
+    return int(load().moe_linear_backward_workspace_size(ctypes.byref(desc)))
+
+
+def moe_linear(desc, x, w, bias, residual, y, z, workspace, stream=None) -> None:
+    _check("moe_linear", load().moe_linear(ctypes.byref(desc), _rp(x), _rp(w), _p(bias), _rp(residual), _rp(y), _rp(z),
+                                           _p(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_linear_backward(desc, x, w, z, dy, dx, dw, db, workspace, stream=None) -> None:
+    """dx, dw and db may each be None."""
+    _check("moe_linear_backward",
+           load().moe_linear_backward(ctypes.byref(desc), _rp(x), _rp(w), _rp(z), _rp(dy), _rp(dx), _p(dw), _p(db),
+                                      _p(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def moe_layer_host_workspace_size(desc: MoELayerDesc, chunks: int = 0) -> int:

@@ -1,0 +1,266 @@
+// linear.cu -- the dense product and its gradients: argument checks, the
+// workspace, the pass that forms dz and db, and the order of the products.
+
+#include <algorithm>
+
+#include "linear.h"
+
+namespace moe {
+
+namespace {
+
+inline size_t al(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+inline bool aligned(const void* p, uintptr_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+struct Lin {                          // the descriptor with its strides filled in
+    int M, N, K, act;
+    bool f32, of32, gf32;             // operands, y / dy, dw
+    long long ld_x, ld_w, ld_y, ld_r, ld_z, ld_dx;
+};
+
+moe_status read_desc(const moe_linear_desc* d, Lin& l)
+{
+    if (!d) return MOE_ERR_INVALID_ARG;
+    if (d->M < 0 || d->N < 1 || d->K < 1) return MOE_ERR_INVALID_ARG;
+    if (d->dtype != MOE_F32 && d->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU) return MOE_ERR_INVALID_ARG;
+    if ((d->out_f32 != 0 && d->out_f32 != 1) || (d->grad_f32 != 0 && d->grad_f32 != 1)) return MOE_ERR_INVALID_ARG;
+    const int ld[6] = {d->ld_x, d->ld_w, d->ld_y, d->ld_r, d->ld_z, d->ld_dx};
+    const int len[6] = {d->K, d->K, d->N, d->N, d->N, d->K};
+    long long v[6];
+    for (int i = 0; i < 6; ++i) {
+        if (ld[i] != 0 && ld[i] < len[i]) return MOE_ERR_INVALID_ARG;
+        v[i] = ld[i] ? ld[i] : len[i];
+    }
+    l = Lin{d->M, d->N, d->K, d->act, d->dtype == MOE_F32, d->dtype == MOE_F32 || d->out_f32 != 0,
+            d->dtype == MOE_F32 || d->grad_f32 != 0, v[0], v[1], v[2], v[3], v[4], v[5]};
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------ dz and db
+// dz = dy act'(z) (written unless dz is null) and the column sums of the
+// unrounded dz.  A block covers 128 columns of a range of rows: a lane holds
+// four columns, the warps take rows in turn; the block's sums go to part
+// [chunks, N] (or straight to db when there is one range).
+constexpr int DZ_THREADS = 256;
+constexpr int DZ_COLS = 128;
+
+struct DzArgs {
+    const void* dy;
+    const void* z;
+    float* dz;
+    float* part;
+    long long ld_dy, ld_z, ld_dz;
+    int M, N, act, rows;         // rows per range
+    int dy_f32, z_f32;
+};
+
+__device__ __forceinline__ float ld1(const void* p, long long i, int f32)
+{
+    return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
+{
+    __shared__ float s[DZ_THREADS / 32][DZ_COLS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = blockIdx.x * DZ_COLS + lane;
+    const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int m = m0 + warp; m < m1; m += DZ_THREADS / 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + 32 * i;
+            if (c >= a.N) continue;
+            float v = ld1(a.dy, (long long)m * a.ld_dy + c, a.dy_f32);
+            if (a.act != MOE_ACT_NONE) v *= act_slope(ld1(a.z, (long long)m * a.ld_z + c, a.z_f32), a.act);
+            acc[i] += v;
+            if (a.dz) a.dz[(long long)m * a.ld_dz + c] = v;
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[warp][lane + 32 * i] = acc[i];
+    __syncthreads();
+    const int c = blockIdx.x * DZ_COLS + threadIdx.x;
+    if (threadIdx.x < DZ_COLS && c < a.N) {
+        float v = 0.f;
+        for (int w = 0; w < DZ_THREADS / 32; ++w) v += s[w][threadIdx.x];
+        a.part[(long long)blockIdx.y * a.N + c] = v;
+    }
+}
+
+__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int chunks, int N, float* db)
+{
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= N) return;
+    float v = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < chunks; ++i) v += part[(long long)i * N + c];
+    db[c] = v;
+}
+
+// Ranges of rows of the dz pass: about four blocks per SM, at least 32 rows each.
+int dz_chunks(const Lin& l, int* rows)
+{
+    const int slices = cdiv(l.N, DZ_COLS);
+    int chunks = std::max(1, std::min(cdiv(l.M, 32), cdiv(4 * 148, slices)));
+    *rows = cdiv(std::max(l.M, 1), chunks);
+    return cdiv(std::max(l.M, 1), *rows);
+}
+
+// dz needs a buffer of its own unless it is dy as it stands.
+bool dz_is_dy(const Lin& l) { return l.act == MOE_ACT_NONE && l.of32 == l.f32; }
+
+struct BwdLayout {
+    size_t dz, part, total;
+};
+
+BwdLayout bwd_layout(const Lin& l)
+{
+    BwdLayout b{0, 0, 0};
+    int rows;
+    b.dz = dz_is_dy(l) ? 0 : al((size_t)l.M * l.N * 4);
+    b.part = al((size_t)dz_chunks(l, &rows) * l.N * 4);
+    b.total = b.dz + b.part;
+    return b;
+}
+
+moe_status zero_rows(void* p, size_t bytes, cudaStream_t st)
+{
+    return cuda_status(cudaMemsetAsync(p, 0, bytes, st));
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int64_t moe_linear_workspace_size(const moe_linear_desc* d)
+{
+    Lin l;
+    if (read_desc(d, l) != MOE_OK) return -1;
+    return 0;
+}
+
+int64_t moe_linear_backward_workspace_size(const moe_linear_desc* d)
+{
+    Lin l;
+    if (read_desc(d, l) != MOE_OK) return -1;
+    return (int64_t)bwd_layout(l).total;
+}
+
+moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* w, const float* bias, const void* residual,
+                      void* y, void* z, void* workspace, size_t ws_bytes, moe_stream_t stream)
+{
+    t_launches = 0;
+    Lin l;
+    const moe_status s = read_desc(d, l);
+    if (s != MOE_OK) return s;
+    if (!w || (l.M > 0 && (!x || !y))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x) || !aligned(w) || !aligned(bias, 4) || !aligned(residual) || !aligned(y) || !aligned(z))
+        return MOE_ERR_INVALID_ARG;
+    if (residual && residual == y && l.ld_r != l.ld_y) return MOE_ERR_INVALID_ARG;
+    const size_t need = (size_t)moe_linear_workspace_size(d);
+    if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace))) return MOE_ERR_WORKSPACE;
+    if (l.M == 0) return MOE_OK;
+    SimtProduct p{};
+    p.P = x;
+    p.Q = w;
+    p.p_rs = l.ld_x;
+    p.q_rs = l.ld_w;
+    p.p_ks = p.q_ks = 1;
+    p.p_f32 = p.q_f32 = l.f32;
+    p.R = l.M;
+    p.C = l.N;
+    p.K = l.K;
+    p.epi = LinEpilogue{bias, residual, z, y, l.ld_y, l.ld_r, l.ld_z, l.act, l.of32, l.f32};
+    return launch_linear_simt(p, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const void* w, const void* z, const void* dy,
+                               void* dx, void* dw, float* db, void* workspace, size_t ws_bytes, moe_stream_t stream)
+{
+    t_launches = 0;
+    Lin l;
+    moe_status s = read_desc(d, l);
+    if (s != MOE_OK) return s;
+    if (!dx && !dw && !db) return MOE_ERR_INVALID_ARG;
+    if (l.M > 0 && (!dy || (dw && !x) || (dx && !w) || (l.act != MOE_ACT_NONE && !z))) return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, w, z, dy, dx, dw};
+    for (const void* p : ptrs)
+        if (!aligned(p)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(db, 4)) return MOE_ERR_INVALID_ARG;
+    const BwdLayout b = bwd_layout(l);
+    if (b.total > 0 && (!workspace || ws_bytes < b.total || !aligned(workspace))) return MOE_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (l.M == 0) {
+        if (dw && (s = zero_rows(dw, (size_t)l.N * l.K * (l.gf32 ? 4 : 2), st)) != MOE_OK) return s;
+        return db ? zero_rows(db, (size_t)l.N * 4, st) : MOE_OK;
+    }
+    float* dz = b.dz ? static_cast<float*>(workspace) : nullptr;
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + b.dz);
+    if (dz || db) {
+        DzArgs a{};
+        a.dy = dy;
+        a.z = z;
+        a.dz = dz;
+        a.ld_dy = l.ld_y;
+        a.ld_z = l.ld_z;
+        a.ld_dz = l.N;
+        a.M = l.M;
+        a.N = l.N;
+        a.act = l.act;
+        a.dy_f32 = l.of32;
+        a.z_f32 = l.f32;
+        const int chunks = dz_chunks(l, &a.rows);
+        a.part = db ? (chunks == 1 ? db : part) : nullptr;
+        linear_dz_kernel<<<dim3(cdiv(l.N, DZ_COLS), chunks), DZ_THREADS, 0, st>>>(a);
+        count_launch();
+        if (db && chunks > 1) {
+            linear_db_kernel<<<cdiv(l.N, 256), 256, 0, st>>>(part, chunks, l.N, db);
+            count_launch();
+        }
+        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    const void* g = dz ? static_cast<const void*>(dz) : dy;
+    const int g_f32 = dz ? 1 : l.of32;
+    const long long ld_g = dz ? l.N : l.ld_y;
+    if (dx) {
+        SimtProduct p{};
+        p.P = g;
+        p.p_rs = ld_g;
+        p.p_ks = 1;
+        p.Q = w;
+        p.q_rs = 1;
+        p.q_ks = l.ld_w;
+        p.p_f32 = g_f32;
+        p.q_f32 = l.f32;
+        p.R = l.M;
+        p.C = l.K;
+        p.K = l.N;
+        p.epi = LinEpilogue{nullptr, nullptr, nullptr, dx, l.ld_dx, 0, 0, MOE_ACT_NONE, l.f32, 0};
+        if ((s = launch_linear_simt(p, st)) != MOE_OK) return s;
+    }
+    if (dw) {
+        SimtProduct p{};
+        p.P = g;
+        p.p_rs = 1;
+        p.p_ks = ld_g;
+        p.Q = x;
+        p.q_rs = 1;
+        p.q_ks = l.ld_x;
+        p.p_f32 = g_f32;
+        p.q_f32 = l.f32;
+        p.R = l.N;
+        p.C = l.K;
+        p.K = l.M;
+        p.epi = LinEpilogue{nullptr, nullptr, nullptr, dw, l.K, 0, 0, MOE_ACT_NONE, l.gf32, 0};
+        if ((s = launch_linear_simt(p, st)) != MOE_OK) return s;
+    }
+    return MOE_OK;
+}
+
+}  // extern "C"

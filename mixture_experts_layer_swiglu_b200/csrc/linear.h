@@ -1,0 +1,81 @@
+// linear.h -- what the dense product's translation units share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "moe.h"
+
+namespace moe {
+
+// What happens to a finished element of out[r, c] (c contiguous in memory):
+// v += bias[c]; z = v; v = act(v) + residual[r, c]; one rounding to the
+// output type.  The gradients use it with all of that off.
+struct LinEpilogue {
+    const float* bias;       // [C] or null
+    const void* residual;    // [R, C], the output's type, or null
+    void* z;                 // [R, C] zt type, or null
+    void* out;               // [R, C]
+    long long ld_out, ld_r, ld_z;
+    int act;
+    int out_f32, z_f32;
+};
+
+// phi and Phi of the exact GELU.  erff is within 2 ulp.
+__device__ __forceinline__ float norm_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678118654752f)); }
+
+__device__ __forceinline__ float act_apply(float z, int act)
+{
+    if (act == MOE_ACT_RELU) return z > 0.f || z != z ? z : 0.f;
+    // below -88 exp overflows and z / inf = -0, as it should be
+    if (act == MOE_ACT_SILU) return z == -INFINITY ? 0.f : z / (1.0f + __expf(-z));
+    if (act == MOE_ACT_GELU) return z == -INFINITY ? 0.f : z * norm_cdf(z);
+    return z;
+}
+
+__device__ __forceinline__ float act_slope(float z, int act)
+{
+    if (act == MOE_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+    if (act == MOE_ACT_SILU) {
+        if (z == -INFINITY) return 0.f;
+        if (z == INFINITY) return 1.f;
+        const float s = 1.0f / (1.0f + __expf(-z));
+        return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    if (act == MOE_ACT_GELU) {
+        if (fabsf(z) == INFINITY) return z > 0.f ? 1.f : 0.f;
+        return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), norm_cdf(z));
+    }
+    return 1.f;
+}
+
+__device__ __forceinline__ void lin_store(const LinEpilogue& e, long long r, int c, float v)
+{
+    if (e.bias) v += e.bias[c];
+    if (e.z) {
+        if (e.z_f32) static_cast<float*>(e.z)[r * e.ld_z + c] = v;
+        else static_cast<__nv_bfloat16*>(e.z)[r * e.ld_z + c] = __float2bfloat16_rn(v);
+    }
+    v = act_apply(v, e.act);
+    if (e.residual)
+        v += e.out_f32 ? static_cast<const float*>(e.residual)[r * e.ld_r + c]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[r * e.ld_r + c]);
+    if (e.out_f32) static_cast<float*>(e.out)[r * e.ld_out + c] = v;
+    else static_cast<__nv_bfloat16*>(e.out)[r * e.ld_out + c] = __float2bfloat16_rn(v);
+}
+
+// out[r, c] = epi(sum_k P(r, k) Q(c, k)), element (r, k) of P at r * p_rs + k * p_ks (one of them 1), Q alike.
+struct SimtProduct {
+    const void* P;
+    const void* Q;
+    long long p_rs, p_ks, q_rs, q_ks;
+    int p_f32, q_f32;
+    int R, C, K;
+    LinEpilogue epi;
+};
+moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st);
+
+}  // namespace moe

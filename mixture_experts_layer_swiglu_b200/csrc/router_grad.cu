@@ -1,0 +1,828 @@
+// router_grad.cu -- training side of the router: the balance loss and z-loss
+// of a routed batch, the gradient of the combine, and the gradient of the
+// router's logits.  Reductions over tokens run in a fixed order (per warp, per
+// block, then over blocks), so equal inputs give equal bits.
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int kMaxE = 256;                   // router rows of the SwiGLU kind
+
+// Sum / maximum over the L lanes of a token's group (L a power of two).
+template <int L>
+__device__ __forceinline__ float group_sum(float v)
+{
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v)
+{
+    // a NaN must survive: fmaxf drops it
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(FULL, v, o);
+        v = (u > v || u != u) ? u : v;
+    }
+    return v;
+}
+
+// ------------------------------------------------------------ balance loss
+struct LossArgs {
+    const float* logits;
+    const int32_t* idx;
+    const uint8_t* mask;
+    const float* weight;
+    int32_t* counts;
+    float* prob_mean;
+    float* losses;
+    float* part_p;        // [blocks, E] sums of the probabilities
+    int32_t* part_c;      // [blocks, E + 1] slot counts and counted tokens
+    float* part_z;        // [blocks] sums of lse^2
+    int T, E, k, blocks, tokens_per_block;
+};
+
+constexpr int LOSS_THREADS = 512;
+constexpr int LOSS_WARPS = LOSS_THREADS / 32;
+
+// Softmax of one token whose logits lie e = l + L * i in the group's lanes.
+// A row of -inf only has p = 0 and lse = 0.
+template <int L, int EPL>
+__device__ __forceinline__ void softmax_row(float (&z)[EPL], float& lse)
+{
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = (z[i] > m || z[i] != z[i]) ? z[i] : m;
+    m = group_max<L>(m);
+    const bool none = m == -INFINITY;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        z[i] = none ? 0.f : __expf(z[i] - m);
+        s += z[i];
+    }
+    s = group_sum<L>(s);
+    const float inv = none ? 0.f : 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) z[i] *= inv;
+    lse = none ? 0.f : m + __logf(s);
+}
+
+// The totals -> the outputs, by one block: sp [E] probability sums, sc [E + 1] counts, z the lse^2 sum.
+__device__ void loss_finish(const LossArgs& a, const float* sp, const int32_t* sc, double zsum)
+{
+    __shared__ double s_red[LOSS_WARPS];
+    const int n = sc[a.E];
+    const double inv = n > 0 ? 1.0 / n : 0.0;
+    double v = 0.0;
+    for (int e = threadIdx.x; e < a.E; e += LOSS_THREADS) {
+        const double pm = sp[e] * inv;
+        a.prob_mean[e] = (float)pm;
+        a.counts[e] = sc[e];
+        v += pm * (sc[e] * inv / a.k) * (a.weight ? a.weight[e] : 1.0);
+    }
+    if (threadIdx.x == 0) a.counts[a.E] = n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int w = 0; w < LOSS_WARPS; ++w) t += s_red[w];
+        a.losses[0] = (float)(t * a.E);
+        a.losses[1] = (float)(zsum * inv);
+    }
+}
+
+// One pass over the logits.  A token is a group of L lanes (L = 8, 16 or 32),
+// each lane EPL of its E logits; a lane keeps the probability sums of its
+// experts in registers over all tokens of its warp, so memory sees each logit
+// once and nothing else but E sums per block.
+template <int L, int EPL>
+__global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossArgs a)
+{
+    __shared__ float s_p[LOSS_WARPS][kMaxE];
+    __shared__ int32_t s_c[kMaxE + 1];
+    __shared__ float s_z[LOSS_WARPS];
+    constexpr int G = 32 / L;                       // tokens per warp and step
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane % L, grp = lane / L;
+    const long long t0 = (long long)blockIdx.x * a.tokens_per_block;
+    const int nt = (int)min((long long)a.tokens_per_block, a.T - t0);
+    for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) s_c[e] = 0;
+    __syncthreads();
+    // counts: the block's slots one by one
+    const long long s0 = t0 * a.k;
+    for (int s = threadIdx.x; s < nt * a.k; s += LOSS_THREADS) {
+        if (a.mask && a.mask[t0 + s / a.k] == 0) continue;
+        const int e = a.idx[s0 + s];
+        if (e < 0 || e >= a.E) set_status(MOE_ERR_DEVICE_BOUNDS);
+        else atomicAdd(&s_c[e], 1);
+    }
+    float acc[EPL], zacc = 0.f;
+    int live_n = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
+    for (int t = warp * G; t < nt; t += LOSS_WARPS * G) {
+        const int tt = t + grp;
+        const bool live = tt < nt && (!a.mask || a.mask[t0 + tt] != 0);
+        const float* row = a.logits + (t0 + tt) * a.E;
+        float z[EPL], lse;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) z[i] = live && l + L * i < a.E ? __ldg(row + l + L * i) : -INFINITY;
+        softmax_row<L, EPL>(z, lse);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) acc[i] += z[i];
+        zacc += lse * lse;
+        live_n += live;
+    }
+    // the groups of a warp, then the warps in order
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) acc[i] += __shfl_xor_sync(FULL, acc[i], o);
+        zacc += __shfl_xor_sync(FULL, zacc, o);
+        live_n += __shfl_xor_sync(FULL, live_n, o);
+    }
+    if (grp == 0)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (l + L * i < a.E) s_p[warp][l + L * i] = acc[i];
+    if (lane == 0) {
+        s_z[warp] = zacc;
+        atomicAdd(&s_c[a.E], live_n);
+    }
+    __syncthreads();
+    const bool alone = a.blocks == 1;
+    for (int e = threadIdx.x; e < a.E; e += LOSS_THREADS) {
+        float v = 0.f;
+        for (int w = 0; w < LOSS_WARPS; ++w) v += s_p[w][e];
+        if (alone) s_p[0][e] = v;
+        else a.part_p[(long long)blockIdx.x * a.E + e] = v;
+    }
+    float zs = 0.f;
+    for (int w = 0; w < LOSS_WARPS; ++w) zs += s_z[w];
+    if (alone) {
+        __syncthreads();
+        loss_finish(a, s_p[0], s_c, zs);
+        return;
+    }
+    for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) a.part_c[(long long)blockIdx.x * (a.E + 1) + e] = s_c[e];
+    if (threadIdx.x == 0) a.part_z[blockIdx.x] = zs;
+}
+
+// The blocks' sums in order of blocks (one block).
+__global__ void __launch_bounds__(LOSS_THREADS) balance_loss_finish_kernel(const LossArgs a)
+{
+    __shared__ float s_p[LOSS_WARPS][kMaxE];
+    __shared__ int32_t s_c[kMaxE + 1];
+    __shared__ double s_z[LOSS_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) s_c[e] = 0;
+    __syncthreads();
+    // each warp the rows b = warp, warp + 16, ...
+    for (int e = lane; e <= a.E; e += 32) {
+        float p = 0.f;
+        int c = 0;
+#pragma unroll 4
+        for (int b = warp; b < a.blocks; b += LOSS_WARPS) {
+            if (e < a.E) p += a.part_p[(long long)b * a.E + e];
+            c += a.part_c[(long long)b * (a.E + 1) + e];
+        }
+        if (e < a.E) s_p[warp][e] = p;
+        atomicAdd(&s_c[e], c);
+    }
+    double z = 0.0;
+    for (int b = warp * 32 + lane; b < a.blocks; b += LOSS_THREADS) z += a.part_z[b];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
+    if (lane == 0) s_z[warp] = z;
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += LOSS_THREADS) {
+        float v = 0.f;
+        for (int w = 0; w < LOSS_WARPS; ++w) v += s_p[w][e];
+        s_p[0][e] = v;
+    }
+    double zs = 0.0;
+    for (int w = 0; w < LOSS_WARPS; ++w) zs += s_z[w];
+    __syncthreads();
+    loss_finish(a, s_p[0], s_c, zs);
+}
+
+// ------------------------------------------------------------ logit gradient
+struct RouteBwdArgs {
+    const float* logits;
+    const int32_t* idx;
+    const float* gate;
+    const float* dgate;
+    const uint8_t* mask;
+    const float* weight;
+    const int32_t* counts;
+    const float* dlosses;
+    float* dlogits;
+    int T, E, k;
+};
+
+constexpr int RB_THREADS = 256;
+constexpr int RB_WARPS = RB_THREADS / 32;
+
+template <int L, int EPL>
+__global__ void __launch_bounds__(RB_THREADS) route_backward_kernel(const RouteBwdArgs a)
+{
+    constexpr int G = 32 / L;
+    // the gate terms of one token, scattered by the lanes that hold its slots
+    __shared__ float s_g[RB_WARPS][G][L * EPL];
+    __shared__ uint8_t s_tag[RB_WARPS][G][L * EPL];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane % L, grp = lane / L;
+    float wf[EPL];
+    float c_bal = 0.f, c_z = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) wf[i] = 0.f;
+    if (a.dlosses) {
+        const int n = a.counts[a.E];
+        const float inv = n > 0 ? 1.0f / (float)n : 0.f;
+        c_bal = a.dlosses[0] * (float)a.E * inv;
+        c_z = 2.0f * a.dlosses[1] * inv;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = l + L * i;
+            if (e < a.E) wf[i] = (float)a.counts[e] * inv / (float)a.k * (a.weight ? a.weight[e] : 1.0f);
+        }
+    }
+    float* sg = s_g[warp][grp];
+    uint8_t* tag = s_tag[warp][grp];
+    for (int i = l; i < L * EPL; i += L) sg[i] = 0.f;
+    __syncwarp();
+    const long long step = (long long)gridDim.x * RB_WARPS * G;
+    for (long long base = ((long long)blockIdx.x * RB_WARPS + warp) * G; base < a.T; base += step) {
+        const long long t = base + grp;
+        const bool live = t < a.T;
+        const bool counted = live && a.dlosses && (!a.mask || a.mask[t] != 0);
+        float z[EPL], d[EPL];
+        const float* row = a.logits + t * a.E;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) z[i] = counted && l + L * i < a.E ? row[l + L * i] : -INFINITY;
+        int e = -1;
+        float g = 0.f, dg = 0.f;
+        if (a.dgate && live && l < a.k) {
+            e = a.idx[t * a.k + l];
+            g = a.gate[t * a.k + l];
+            dg = a.dgate[t * a.k + l];
+            if (e < 0 || e >= a.E) { set_status(MOE_ERR_DEVICE_BOUNDS); e = -1; }
+        }
+        if (a.dlosses) {
+            float lse, dot = 0.f;
+            softmax_row<L, EPL>(z, lse);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) dot += z[i] * wf[i];
+            dot = group_sum<L>(dot);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] = z[i] * (c_bal * (wf[i] - dot) + c_z * lse);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] = 0.f;
+        }
+        if (a.dgate) {
+            const float mean = group_sum<L>(g * dg);
+            const float v = g * (dg - mean);
+            // a router's ids are distinct; should two be equal (the tag of one is
+            // overwritten by the other's), the slots are added one after the other
+            if (e >= 0) tag[e] = (uint8_t)l;
+            __syncwarp();
+            const bool clash = e >= 0 && tag[e] != (uint8_t)l;
+            if (__any_sync(FULL, clash)) {
+                for (int j = 0; j < a.k; ++j) {
+                    if (l == j && e >= 0) sg[e] += v;
+                    __syncwarp();
+                }
+            } else if (e >= 0) {
+                sg[e] = v;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] += sg[l + L * i];
+            __syncwarp();
+            if (e >= 0) sg[e] = 0.f;
+            __syncwarp();
+        }
+        float* out = a.dlogits + t * a.E;
+        if (live)
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (l + L * i < a.E) out[l + L * i] = d[i];
+    }
+}
+
+// ------------------------------------------------------------ combine gradient
+struct CombineBwdArgs {
+    const void* dy;
+    const float* ys;
+    const int32_t* offsets;
+    const int32_t* row_of;
+    const int32_t* idx;
+    const float* gate;
+    const float* cmix;
+    const void* cvec;
+    const void* x;
+    float* dgate;
+    void* dys;
+    void* dx;
+    float* dcmix;
+    float* dcvec;
+    int T, d, k, n_ffn, n_shared, n_zero, n_copy, n_const;
+    long long rows_cap;
+};
+
+template <typename T>
+__device__ __forceinline__ void ld8(const T* p, float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(w[i]); v[2 * i + 1] = bf16_hi(w[i]); }
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void st8(T* p, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                  pack_bf16(v[6], v[7]));
+    } else {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8])
+{
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+    return s;
+}
+
+constexpr int CB_SPLIT = 4;                  // warps per token
+constexpr int CB_TOKENS = 2;                 // tokens per block
+constexpr int CB_THREADS = CB_SPLIT * CB_TOKENS * 32;
+constexpr int CB_C = 2;                      // 8-element chunks per lane and step
+constexpr int CB_MAXK = 32;
+
+// A token's row is split over 4 warps; each lane holds its chunks of dy in
+// registers and goes over the slots: one read of the expert's row for the dot
+// product, one write of the gated row.
+template <typename T, typename TO>
+__global__ void __launch_bounds__(CB_THREADS) combine_backward_kernel(const CombineBwdArgs a)
+{
+    __shared__ int s_e[CB_TOKENS][CB_MAXK], s_r[CB_TOKENS][CB_MAXK];
+    __shared__ float s_g[CB_TOKENS][CB_MAXK], s_a1[CB_TOKENS][CB_MAXK], s_a2[CB_TOKENS][CB_MAXK];
+    __shared__ float s_dot[CB_TOKENS][CB_MAXK + 1][CB_SPLIT];       // slot dot products; [k]: <dy, x>
+    __shared__ float s_coef[CB_TOKENS];
+    const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5;
+    const int tib = wib / CB_SPLIT, part = wib % CB_SPLIT;
+    const int copy0 = a.n_ffn + a.n_zero, const0 = copy0 + a.n_copy, n_ids = const0 + a.n_const;
+    const int vecs = a.d / 8, per = cdiv(vecs, CB_SPLIT);
+    const int i0 = part * per, i1 = min(vecs, i0 + per);
+    const bool want_dot = a.dgate || a.dcmix;
+    const TO* dy = reinterpret_cast<const TO*>(a.dy);
+    const T* x = reinterpret_cast<const T*>(a.x);
+    const T* cvec = reinterpret_cast<const T*>(a.cvec);
+    T* dys = reinterpret_cast<T*>(a.dys);
+    for (long long base = (long long)blockIdx.x * CB_TOKENS; base < a.T; base += (long long)gridDim.x * CB_TOKENS) {
+        const long long t = base + tib;
+        const bool live = t < a.T;
+        if (part == 0) {
+            int e = -1, r = -1;
+            float g = 0.f, a1 = 0.f, a2 = 0.f, coef = 0.f;
+            if (live && lane < a.k) {
+                e = a.idx[t * a.k + lane];
+                g = a.gate[t * a.k + lane];
+                bool bad = e < 0 || e >= n_ids;
+                if (!bad && e < a.n_ffn) {
+                    r = a.row_of[t * a.k + lane];
+                    bad = r < 0 || r >= a.rows_cap;
+                }
+                if (bad) { set_status(MOE_ERR_DEVICE_BOUNDS); e = -1; }
+                if (e >= copy0 && e < const0) coef = g;
+                if (e >= const0 && a.cmix) {
+                    a1 = a.cmix[(t * a.n_const + (e - const0)) * 2 + 0];
+                    a2 = a.cmix[(t * a.n_const + (e - const0)) * 2 + 1];
+                    coef = g * a1;
+                }
+            }
+            coef = group_sum<32>(coef);
+            s_e[tib][lane] = e;
+            s_r[tib][lane] = r;
+            s_g[tib][lane] = g;
+            s_a1[tib][lane] = a1;
+            s_a2[tib][lane] = a2;
+            if (lane == 0) s_coef[tib] = coef;
+        }
+        for (int j = lane; j <= a.k; j += 32) s_dot[tib][j][part] = 0.f;
+        __syncthreads();
+        if (live) {
+            bool need_x = false;
+            if (want_dot && a.n_copy + a.n_const > 0)
+                for (int j = 0; j < a.k; ++j) need_x |= s_e[tib][j] >= copy0;
+            for (int ib = i0; ib < i1; ib += 32 * CB_C) {
+                float v[CB_C][8];
+#pragma unroll
+                for (int c = 0; c < CB_C; ++c) {
+                    const int i = ib + lane + 32 * c;
+                    if (i < i1) ld8(dy + t * a.d + i * 8, v[c]);
+                    else
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[c][q] = 0.f;
+                }
+                if (need_x) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int c = 0; c < CB_C; ++c) {
+                        const int i = ib + lane + 32 * c;
+                        float u[8];
+                        if (i < i1) { ld8(x + t * a.d + i * 8, u); s += dot8(u, v[c]); }
+                    }
+                    s = group_sum<32>(s);
+                    if (lane == 0) s_dot[tib][a.k][part] += s;
+                }
+                for (int j = 0; j < a.k; ++j) {
+                    const int e = s_e[tib][j];
+                    const float g = s_g[tib][j];
+                    float s = 0.f;
+                    if (e >= 0 && e < a.n_ffn) {
+                        const long long r = s_r[tib][j];
+#pragma unroll
+                        for (int c = 0; c < CB_C; ++c) {
+                            const int i = ib + lane + 32 * c;
+                            if (i >= i1) continue;
+                            if (a.dgate) {
+                                float u[8];
+                                ld8(a.ys + r * a.d + i * 8, u);
+                                s += dot8(u, v[c]);
+                            }
+                            if (dys) {
+                                float u[8];
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) u[q] = g * v[c][q];
+                                st8(dys + r * a.d + i * 8, u);
+                            }
+                        }
+                        if (!a.dgate) continue;
+                    } else if (e >= const0 && want_dot) {
+#pragma unroll
+                        for (int c = 0; c < CB_C; ++c) {
+                            const int i = ib + lane + 32 * c;
+                            float u[8];
+                            if (i < i1) { ld8(cvec + (long long)(e - const0) * a.d + i * 8, u); s += dot8(u, v[c]); }
+                        }
+                    } else {
+                        continue;
+                    }
+                    s = group_sum<32>(s);
+                    if (lane == 0) s_dot[tib][j][part] += s;
+                }
+                if (dys)
+                    for (int sh = 0; sh < a.n_shared; ++sh) {
+                        const long long r = (long long)a.offsets[a.n_ffn + sh] + t;
+                        if (r < 0 || r >= a.rows_cap) { set_status(MOE_ERR_DEVICE_BOUNDS); continue; }
+#pragma unroll
+                        for (int c = 0; c < CB_C; ++c) {
+                            const int i = ib + lane + 32 * c;
+                            if (i < i1) st8(dys + r * a.d + i * 8, v[c]);
+                        }
+                    }
+                if (a.dx) {
+                    const float cf = s_coef[tib];
+#pragma unroll
+                    for (int c = 0; c < CB_C; ++c) {
+                        const int i = ib + lane + 32 * c;
+                        if (i >= i1) continue;
+                        float u[8];
+                        // a token without such slots gets zeros, also where dy is not finite
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) u[q] = cf == 0.f ? 0.f : cf * v[c][q];
+                        st8(reinterpret_cast<T*>(a.dx) + t * a.d + i * 8, u);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (live && part == 0) {
+            float dot[2] = {0.f, 0.f};              // the slot's own, and <dy, x>
+            if (lane < a.k)
+                for (int q = 0; q < CB_SPLIT; ++q) dot[0] += s_dot[tib][lane][q];
+            for (int q = 0; q < CB_SPLIT; ++q) dot[1] += s_dot[tib][a.k][q];
+            if (a.dgate && lane < a.k) {
+                const int e = s_e[tib][lane];
+                float v = 0.f;
+                if (e >= const0) v = s_a1[tib][lane] * dot[1] + s_a2[tib][lane] * dot[0];
+                else if (e >= copy0) v = dot[1];
+                else if (e >= 0 && e < a.n_ffn) v = dot[0];
+                a.dgate[t * a.k + lane] = v;
+            }
+            if (a.dcmix)
+                for (int c = lane; c < a.n_const; c += 32) {
+                    float gs = 0.f, on = 0.f;
+                    for (int j = 0; j < a.k; ++j)
+                        if (s_e[tib][j] == const0 + c) {
+                            gs += s_g[tib][j];
+                            on = 0.f;
+                            for (int q = 0; q < CB_SPLIT; ++q) on += s_dot[tib][j][q];
+                        }
+                    a.dcmix[(t * a.n_const + c) * 2 + 0] = gs == 0.f ? 0.f : gs * dot[1];
+                    a.dcmix[(t * a.n_const + c) * 2 + 1] = gs == 0.f ? 0.f : gs * on;
+                }
+        }
+        __syncthreads();
+    }
+}
+
+// dconst_vec[c] = sum over the slots of constant expert c of g a2 dy_t.  A
+// cluster of 8 blocks shares one (256 columns, c): each block lists the
+// matching slots of its token range in order and sums their rows, then the
+// blocks' sums are added in order.
+constexpr int CV_CLUSTER = 8;
+constexpr int CV_THREADS = 256;
+
+template <typename TO>
+__global__ void __launch_bounds__(CV_THREADS) const_vec_grad_kernel(const CombineBwdArgs a)
+{
+    __shared__ float s_acc[CV_THREADS];
+    __shared__ float s_w[CV_THREADS];
+    __shared__ int s_t[CV_THREADS];
+    __shared__ int s_n[CV_THREADS / 32 + 1];
+    const int rank = blockIdx.x % CV_CLUSTER, slice = blockIdx.x / CV_CLUSTER, c = blockIdx.y;
+    const int id = a.n_ffn + a.n_zero + a.n_copy + c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = slice * CV_THREADS + threadIdx.x;
+    const long long S = (long long)a.T * a.k;
+    const long long s0 = S * rank / CV_CLUSTER, s1 = S * (rank + 1) / CV_CLUSTER;
+    const TO* dy = reinterpret_cast<const TO*>(a.dy);
+    float acc = 0.f;
+    for (long long b = s0; b < s1; b += CV_THREADS) {
+        const long long s = b + threadIdx.x;
+        const bool hit = s < s1 && a.idx[s] == id;
+        const unsigned m = __ballot_sync(FULL, hit);
+        if (lane == 0) s_n[warp] = __popc(m);
+        __syncthreads();
+        int before = 0, total = 0;
+        for (int w = 0; w < CV_THREADS / 32; ++w) {
+            before += w < warp ? s_n[w] : 0;
+            total += s_n[w];
+        }
+        if (hit) {
+            const int at = before + __popc(m & ((1u << lane) - 1u));
+            const int t = (int)(s / a.k);
+            s_t[at] = t;
+            s_w[at] = a.gate[s] * a.cmix[((long long)t * a.n_const + c) * 2 + 1];
+        }
+        __syncthreads();
+        if (col < a.d)
+#pragma unroll 8
+            for (int i = 0; i < total; ++i) acc = fmaf(s_w[i], (float)dy[(long long)s_t[i] * a.d + col], acc);
+        __syncthreads();
+    }
+    s_acc[threadIdx.x] = acc;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    if (rank == 0 && col < a.d) {
+        float v = 0.f;
+        for (int q = 0; q < CV_CLUSTER; ++q) v += cl.map_shared_rank(s_acc, q)[threadIdx.x];
+        a.dcvec[(long long)c * a.d + col] = v;
+    }
+    cl.sync();
+}
+
+// ------------------------------------------------------------ launches
+inline bool aligned(const void* p, uintptr_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline size_t al(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+inline int router_rows(const moe_layer_desc* d) { return d->n_ffn + d->n_zero + d->n_copy + d->n_const; }
+
+// Blocks of the loss pass: one up to 1024 tokens' worth of lanes (the second
+// launch costs more than the pass), then enough tokens per block that its fixed
+// part does not count, at most two blocks per SM.
+void loss_blocks(int T, int E, int& blocks, int& per)
+{
+    const long long lanes = (long long)T * (E <= 8 ? 8 : E <= 16 ? 16 : 32);
+    const long long want = (lanes + 8 * LOSS_THREADS - 1) / (8 * LOSS_THREADS);
+    blocks = (int)std::max<long long>(1, std::min<long long>(want, 296));
+    per = (T + blocks - 1) / blocks;
+    blocks = std::max(1, (T + per - 1) / std::max(per, 1));
+}
+
+#define MOE_LANES(E, CALL)                                 \
+    do {                                                   \
+        if ((E) <= 8) { CALL(8, 1); }                      \
+        else if ((E) <= 16) { CALL(16, 1); }               \
+        else if ((E) <= 32) { CALL(32, 1); }               \
+        else if ((E) <= 64) { CALL(32, 2); }               \
+        else if ((E) <= 128) { CALL(32, 4); }              \
+        else { CALL(32, 8); }                              \
+    } while (0)
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int64_t moe_balance_loss_workspace_size(const moe_layer_desc* d)
+{
+    if (validate_desc(d) != MOE_OK || d->kind != MOE_EXPERT_SWIGLU) return -1;
+    const int E = router_rows(d);
+    int blocks, per;
+    loss_blocks(d->T, E, blocks, per);
+    return (int64_t)(al((size_t)blocks * E * 4) + al((size_t)blocks * (E + 1) * 4) + al((size_t)blocks * 4));
+}
+
+moe_status moe_balance_loss(const moe_layer_desc* d, const float* logits, const int32_t* topk_idx,
+                            const uint8_t* token_mask, const float* expert_weight, int32_t* counts, float* prob_mean,
+                            float* losses, void* workspace, size_t ws_bytes, moe_stream_t stream)
+{
+    t_launches = 0;
+    const moe_status s = validate_desc(d);
+    if (s != MOE_OK) return s;
+    if (d->kind != MOE_EXPERT_SWIGLU) return MOE_ERR_UNSUPPORTED;
+    if (!counts || !prob_mean || !losses || (d->T > 0 && (!logits || !topk_idx))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits) || !aligned(topk_idx, 4) || !aligned(expert_weight, 4) || !aligned(counts, 4) ||
+        !aligned(prob_mean, 4) || !aligned(losses, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < (size_t)moe_balance_loss_workspace_size(d) || !aligned(workspace))
+        return MOE_ERR_WORKSPACE;
+    LossArgs a{};
+    a.logits = logits;
+    a.idx = topk_idx;
+    a.mask = token_mask;
+    a.weight = expert_weight;
+    a.counts = counts;
+    a.prob_mean = prob_mean;
+    a.losses = losses;
+    a.T = d->T;
+    a.E = router_rows(d);
+    a.k = d->top_k;
+    loss_blocks(a.T, a.E, a.blocks, a.tokens_per_block);
+    char* p = static_cast<char*>(workspace);
+    a.part_p = reinterpret_cast<float*>(p);
+    p += al((size_t)a.blocks * a.E * 4);
+    a.part_c = reinterpret_cast<int32_t*>(p);
+    p += al((size_t)a.blocks * (a.E + 1) * 4);
+    a.part_z = reinterpret_cast<float*>(p);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define CALL(L, EPL) balance_loss_kernel<L, EPL><<<a.blocks, LOSS_THREADS, 0, st>>>(a)
+    MOE_LANES(a.E, CALL);
+#undef CALL
+    count_launch();
+    if (a.blocks > 1) {
+        balance_loss_finish_kernel<<<1, LOSS_THREADS, 0, st>>>(a);
+        count_launch();
+    }
+    return cuda_status(cudaGetLastError());
+}
+
+moe_status moe_route_backward(const moe_layer_desc* d, const float* logits, const int32_t* topk_idx,
+                              const float* topk_gate, const float* dgate, const uint8_t* token_mask,
+                              const float* expert_weight, const int32_t* counts, const float* dlosses, float* dlogits,
+                              moe_stream_t stream)
+{
+    t_launches = 0;
+    const moe_status s = validate_desc(d);
+    if (s != MOE_OK) return s;
+    if (d->kind != MOE_EXPERT_SWIGLU) return MOE_ERR_UNSUPPORTED;
+    if (!dgate && !dlosses) return MOE_ERR_INVALID_ARG;
+    if (d->T > 0 && (!dlogits || (dlosses && (!logits || !counts)) || (dgate && (!topk_idx || !topk_gate))))
+        return MOE_ERR_INVALID_ARG;
+    const void* four[] = {topk_idx, topk_gate, dgate, expert_weight, counts, dlosses};
+    for (const void* p : four)
+        if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits) || !aligned(dlogits)) return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) return MOE_OK;
+    RouteBwdArgs a{};
+    a.logits = logits;
+    a.idx = topk_idx;
+    a.gate = topk_gate;
+    a.dgate = dgate;
+    a.mask = token_mask;
+    a.weight = expert_weight;
+    a.counts = counts;
+    a.dlosses = dlosses;
+    a.dlogits = dlogits;
+    a.T = d->T;
+    a.E = router_rows(d);
+    a.k = d->top_k;
+    const int G = a.E <= 8 ? 4 : a.E <= 16 ? 2 : 1;
+    const int blocks = (int)std::min<long long>(((long long)a.T + RB_WARPS * G - 1) / (RB_WARPS * G), 8ll * num_sms());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define CALL(L, EPL) route_backward_kernel<L, EPL><<<blocks, RB_THREADS, 0, st>>>(a)
+    MOE_LANES(a.E, CALL);
+#undef CALL
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+moe_status moe_combine_backward(const moe_layer_desc* d, const moe_layer_weights* w, const void* dy,
+                                const void* y_sorted, const int32_t* expert_offsets, const int32_t* row_of,
+                                const int32_t* topk_idx, const float* topk_gate, const float* const_mix, const void* x,
+                                float* dgate, void* dy_sorted, void* dx, float* dconst_mix, float* dconst_vec,
+                                moe_stream_t stream)
+{
+    t_launches = 0;
+    const moe_status s = validate_desc(d);
+    if (s != MOE_OK) return s;
+    if (d->kind != MOE_EXPERT_SWIGLU) return MOE_ERR_UNSUPPORTED;
+    if (!w || (!dgate && !dy_sorted && !dx && !dconst_mix && !dconst_vec)) return MOE_ERR_INVALID_ARG;
+    if (d->n_const == 0 && (dconst_mix || dconst_vec)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool mix = d->n_const > 0 && (dgate || dx || dconst_mix || dconst_vec);
+    if (d->T > 0) {
+        if (!dy || !topk_idx || !topk_gate || (d->n_ffn > 0 && !row_of)) return MOE_ERR_INVALID_ARG;
+        if (dgate && d->n_ffn > 0 && !y_sorted) return MOE_ERR_INVALID_ARG;
+        if ((dgate || dconst_mix) && d->n_copy + d->n_const > 0 && !x) return MOE_ERR_INVALID_ARG;
+        if (mix && !const_mix) return MOE_ERR_INVALID_ARG;
+        if (d->n_const > 0 && (dgate || dconst_mix) && !w->const_vec) return MOE_ERR_INVALID_ARG;
+        if (dy_sorted && d->n_shared > 0 && !expert_offsets) return MOE_ERR_INVALID_ARG;
+        const void* vec[] = {dy, y_sorted, x, dy_sorted, dx, w->const_vec};
+        for (const void* p : vec)
+            if (!aligned(p)) return MOE_ERR_INVALID_ARG;
+    }
+    const void* four[] = {expert_offsets, row_of, topk_idx, topk_gate, const_mix, dgate, dconst_mix, dconst_vec};
+    for (const void* p : four)
+        if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
+    if (d->T == 0) {
+        if (dconst_vec && cudaMemsetAsync(dconst_vec, 0, (size_t)d->n_const * d->d_model * 4, st) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    CombineBwdArgs a{};
+    a.dy = dy;
+    a.ys = static_cast<const float*>(y_sorted);
+    a.offsets = expert_offsets;
+    a.row_of = row_of;
+    a.idx = topk_idx;
+    a.gate = topk_gate;
+    a.cmix = mix ? const_mix : nullptr;
+    a.cvec = w->const_vec;
+    a.x = x;
+    a.dgate = dgate;
+    a.dys = dy_sorted;
+    a.dx = dx;
+    a.dcmix = dconst_mix;
+    a.dcvec = dconst_vec;
+    a.T = d->T;
+    a.d = d->d_model;
+    a.k = d->top_k;
+    a.n_ffn = d->n_ffn;
+    a.n_shared = d->n_shared;
+    a.n_zero = d->n_zero;
+    a.n_copy = d->n_copy;
+    a.n_const = d->n_const;
+    a.rows_cap = moe_row_capacity(d);
+    const bool f32 = d->dtype == MOE_F32, dyf = f32 || d->out_f32;
+    if (dgate || dy_sorted || dx || dconst_mix) {
+        const int blocks = (int)std::min<long long>(((long long)a.T + CB_TOKENS - 1) / CB_TOKENS, 64ll * num_sms());
+        if (f32) combine_backward_kernel<float, float><<<blocks, CB_THREADS, 0, st>>>(a);
+        else if (dyf) combine_backward_kernel<__nv_bfloat16, float><<<blocks, CB_THREADS, 0, st>>>(a);
+        else combine_backward_kernel<__nv_bfloat16, __nv_bfloat16><<<blocks, CB_THREADS, 0, st>>>(a);
+        count_launch();
+        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    if (dconst_vec) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(CV_CLUSTER * cdiv(a.d, CV_THREADS), a.n_const);
+        cfg.blockDim = dim3(CV_THREADS);
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {CV_CLUSTER, 1, 1};
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        const cudaError_t e = dyf ? cudaLaunchKernelEx(&cfg, const_vec_grad_kernel<float>, a)
+                                  : cudaLaunchKernelEx(&cfg, const_vec_grad_kernel<__nv_bfloat16>, a);
+        count_launch();
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -88,6 +88,24 @@ class StageBuffers:
         self.y = torch.empty((T, d), dtype=out_dtype(desc), device=device)
 
 
+class RouterGradBuffers:
+    """Device buffers of the balance loss and the router's gradient (moe_balance_loss,
+    moe_combine_backward, moe_route_backward)."""
+
+    def __init__(self, desc: abi.MoELayerDesc, device="cuda"):
+        need = abi.moe_balance_loss_workspace_size(desc)
+        if need < 0:
+            raise abi.MoEError("moe_balance_loss_workspace_size", abi.MOE_ERR_INVALID_ARG)
+        T, E = desc.T, router_width(desc)
+        f32 = dict(dtype=torch.float32, device=device)
+        self.counts = torch.empty((E + 1,), dtype=torch.int32, device=device)   # slots per expert, then counted tokens
+        self.prob_mean = torch.empty((E,), **f32)
+        self.losses = torch.empty((2,), **f32)                                  # balance loss, z-loss
+        self.dgate = torch.empty((T, desc.top_k), **f32)
+        self.dlogits = torch.empty((T, E), **f32)
+        self.workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+
+
 def run_stages(desc, weights, x, bufs: StageBuffers, prev_logits=None, stream=None, want_logits=True):
     """moe_route -> moe_permute -> moe_grouped_ffn -> moe_combine into bufs.y."""
     b = bufs

@@ -1,0 +1,331 @@
+"""The dense product (moe_linear, moe_linear_backward) against its formula in
+64 bits.
+
+Tolerances.  u = 2^-24 is half a step of fp32 and h = torch.finfo(bf16).eps / 2
+= 2^-8 half a step of bf16, both relative.  A sum of K products held in fp32
+is off by at most 2 u per addition (one step, whatever the order and the
+rounding direction), so by 2 (K + 2) u (|x| |w|^T + |b|).  The activations'
+slopes are at most 1.13, and their own error at most |z| (4 + 1.2 |z|) 2^-23
+(the fast exponential is off by 2 + 1.17 |z| steps).  A bf16 result adds
+h |result| for its rounding; in the backward pass the rounding of dz to bf16
+adds h |dz| |w|.  Since a bf16 result's neighbours are a full step apart, a
+value that the fp32 error moves over a rounding border is still within these
+bounds (the rounding is applied to the moved value).
+"""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import mixture_experts_layer_swiglu_b200 as moe
+
+U, H = 2.0 ** -24, torch.finfo(torch.bfloat16).eps / 2
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    moe.moe_get_device_status(reset=True)
+    yield
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status(reset=True) == moe.MOE_OK
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _mat(g, rows, cols, dtype, std=1.0, pad=0):
+    return (torch.randn((rows, cols + pad), device="cuda", generator=g) * std).to(dtype)[:, :cols]
+
+
+def _act(z, act):
+    return {"none": lambda: z, "relu": lambda: z.clamp(min=0), "silu": lambda: z * torch.sigmoid(z),
+            "gelu": lambda: z * torch.special.ndtr(z)}[act]()
+
+
+def _slope(z, act):
+    if act == "none":
+        return torch.ones_like(z)
+    if act == "relu":
+        return (z > 0).double()
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return s * (1 + z * (1 - s))
+    return torch.special.ndtr(z) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+
+
+def _act_err(z):
+    return z.abs() * (4 + 1.2 * z.abs()) * 2.0 ** -23
+
+
+def _round(dtype):
+    return H if dtype == torch.bfloat16 else U
+
+
+def _close(name, got, want, bound):
+    got = got.double()
+    assert got.shape == want.shape
+    bad = ~((got - want).abs() <= bound + 1e-37)
+    assert not bad.any(), (f"{name}: {int(bad.sum())} of {bad.numel()} beyond the bound, worst "
+                           f"{float(((got - want).abs() / (bound + 1e-37)).max()):.2f} of it")
+
+
+def _forward(M, N, K, dtype, act, out_f32=False, bias=True, residual=True, save=True, pad=0, seed=0):
+    g, dt = _gen(seed), DT[dtype]
+    out = torch.float32 if out_f32 else dt
+    x, w = _mat(g, M, K, dt, pad=pad), _mat(g, N, K, dt, K ** -0.5, pad=pad)
+    b = torch.randn(N, device="cuda", generator=g) if bias else None
+    r = _mat(g, M, N, out, pad=pad) if residual else None
+    desc = moe.make_linear_desc(M, N, K, dtype, act, out_f32=out_f32, ld_w=K + pad)
+    # poisoned, in rows of a wider buffer: what lies beside the rows must stay
+    ybuf = torch.full((M, N + pad), 777.0, device="cuda", dtype=out)
+    zbuf = torch.full((M, N + pad), 777.0, device="cuda", dtype=dt)
+    z = zbuf[:, :N] if save else None
+    y = moe.Linear(desc, w, b).forward(x, residual=r, y=ybuf[:, :N], z=z)
+    z64 = x.double() @ w.double().T + (b.double() if bias else 0)
+    mag = x.double().abs() @ w.double().abs().T + (b.double().abs() if bias else 0)
+    ez = 2 * (K + 2) * U * mag
+    y64 = _act(z64, act) + (r.double() if residual else 0)
+    ey = 1.13 * ez + _act_err(z64) + 2 * U * y64.abs()
+    _close("y", y, y64, ey + _round(out) * (y64.abs() + ey))
+    if save:
+        _close("z", z, z64, ez + _round(dt) * (z64.abs() + ez))
+    if pad:
+        assert (ybuf[:, N:] == 777.0).all() and (not save or (zbuf[:, N:] == 777.0).all())
+
+
+SIZES = [(1, 8, 8), (1, 1, 1), (1, 4096, 512), (2, 33, 17), (7, 129, 65), (16, 256, 1024), (17, 130, 200), (64, 256, 128),
+         (127, 128, 64), (128, 128, 128), (129, 257, 72), (200, 77, 1411), (333, 1029, 264), (600, 512, 2048),
+         (1100, 384, 320), (2049, 24, 512)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_forward_sizes(M, N, K, dtype):
+    _forward(M, N, K, dtype, "gelu", seed=M + N)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("bias,residual,save,out_f32", [(False, False, False, False), (True, False, True, True),
+                                                        (False, True, False, True), (True, True, True, False)])
+def test_forward_epilogues(dtype, act, bias, residual, save, out_f32):
+    _forward(150, 200, 136, dtype, act, out_f32, bias, residual, save)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", [8, 5, 24])
+def test_forward_row_strides(dtype, pad):
+    _forward(70, 136, 200, dtype, "silu", pad=pad)
+    _forward(300, 520, 333, dtype, "none", pad=pad)
+
+
+def test_forward_large():
+    _forward(4096, 2816, 1024, "bf16", "silu", save=False)
+    _forward(5000, 3001, 1024, "bf16", "none", residual=False, save=False, out_f32=True)
+
+
+@pytest.mark.parametrize("N", [8, 20, 64, 256])
+def test_router_logits_with_the_gating_residual(N):
+    _forward(4097, N, 2048, "bf16", "none", out_f32=True, save=False)
+
+
+def test_residual_in_place():
+    g = _gen(3)
+    x, w = _mat(g, 260, 512, torch.bfloat16), _mat(g, 384, 512, torch.bfloat16, 0.05)
+    r = _mat(g, 260, 384, torch.bfloat16)
+    layer = moe.Linear(moe.make_linear_desc(260, 384, 512, act="silu"), w)
+    want = layer.forward(x, residual=r)
+    same = r.clone()
+    layer.forward(x, residual=same, y=same)
+    assert torch.equal(want, same)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_non_finite_inputs_stay_in_their_rows_and_columns(dtype):
+    g, dt = _gen(4), DT[dtype]
+    x, w = _mat(g, 70, 200, dt), _mat(g, 140, 200, dt, 0.1)
+    x[3, 5], x[69, 199], w[139, 0] = float("nan"), float("inf"), float("nan")
+    y = moe.Linear(moe.make_linear_desc(70, 140, 200, dtype), w).forward(x).float()
+    assert y[3].isnan().all() and y[:, 139].isnan().all()
+    assert not y[69, :139].isfinite().any()
+    keep = [i for i in range(69) if i != 3]
+    assert y[keep][:, :139].isfinite().all()
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_activations_at_their_ends(act):
+    """x = one-hot rows, so z is w exactly: the largest and smallest values, zeros and infinities."""
+    vals = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 90.0, -90.0, 200.0, -200.0, 3e38, -3e38, float("inf"), -float("inf")],
+                        device="cuda")
+    w = vals[:, None].contiguous()
+    x = torch.ones((1, 1), device="cuda")
+    layer = moe.Linear(moe.make_linear_desc(1, 12, 1, "f32", act), w)
+    y = layer.forward(x).double()[0]
+    want = _act(vals.double(), act)
+    want[11] = 0.0                                     # -inf: the limit
+    fin = want.isfinite()
+    assert torch.equal(y[~fin], want[~fin])
+    assert ((y - want)[fin].abs() <= 1e-6 * want[fin].abs() + 1e-36).all()
+    dx, dw, _ = layer.backward(x, torch.ones((1, 12), device="cuda"), z=vals[None], need_dx=False)
+    slope = _slope(vals.double(), act)
+    slope[10], slope[11] = 1.0, 0.0
+    assert ((dw.double()[:, 0] - slope).abs() <= 1e-5).all()
+
+
+def _backward(M, N, K, dtype, act, out_f32=False, grad_f32=False, pad=0, seed=0):
+    g, dt = _gen(seed), DT[dtype]
+    out = torch.float32 if out_f32 else dt
+    x, w = _mat(g, M, K, dt, pad=pad), _mat(g, N, K, dt, K ** -0.5, pad=pad)
+    dy = _mat(g, M, N, out, pad=pad)
+    z = _mat(g, M, N, dt, pad=pad) if act != "none" else None
+    desc = moe.make_linear_desc(M, N, K, dtype, act, out_f32=out_f32, grad_f32=grad_f32, ld_w=K + pad)
+    dxbuf = torch.full((M, K + pad), 777.0, device="cuda", dtype=dt)
+    dx, dw, db = moe.Linear(desc, w).backward(x, dy, z=z, dx=dxbuf[:, :K], need_db=True)
+    assert dw.dtype == (torch.float32 if grad_f32 else dt) and db.dtype == torch.float32
+    dz = dy.double()
+    ed = torch.zeros_like(dz)                          # error of the unrounded dz
+    if act != "none":
+        zz = z.double()
+        dz = dz * _slope(zz, act)
+        ed = dy.double().abs() * (8 + 1.2 * zz.abs() + zz * zz) * (1 + zz.abs()) * 2.0 ** -23 + 2 * U * dz.abs()
+    exact = act == "none" and out == dt
+    er = ed if exact or dtype == "f32" else ed + H * (dz.abs() + ed)          # ... and of the rounded one
+    mag = dz.abs() + ed
+    wd, xd = w.double(), x.double()
+    ex = er @ wd.abs() + 2 * (N + 2) * U * (mag @ wd.abs())
+    _close("dx", dx, dz @ wd, ex + _round(dt) * ((dz @ wd).abs() + ex))
+    ew = (ed + 2 * U * dz.abs() if grad_f32 else er).T @ xd.abs() + 2 * (3 * M + 2) * U * (mag.T @ xd.abs())
+    want = dz.T @ xd
+    _close("dw", dw, want, ew + _round(dw.dtype) * (want.abs() + ew))
+    _close("db", db, dz.sum(0), ed.sum(0) + 2 * (M + 2) * U * mag.sum(0))
+    if pad:
+        assert (dxbuf[:, K:] == 777.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_backward_sizes(M, N, K, dtype):
+    _backward(M, N, K, dtype, "silu", seed=M + N)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("out_f32", [False, True])
+@pytest.mark.parametrize("grad_f32", [False, True])
+def test_backward_types(dtype, act, out_f32, grad_f32):
+    _backward(300, 136, 200, dtype, act, out_f32, grad_f32)
+    _backward(257, 20, 512, dtype, act, out_f32, grad_f32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", [8, 5])
+def test_backward_row_strides(dtype, pad):
+    _backward(150, 136, 200, dtype, "gelu", pad=pad)
+    _backward(150, 136, 200, dtype, "none", pad=pad)
+    _backward(530, 333, 260, dtype, "none", out_f32=True, grad_f32=True, pad=pad)
+
+
+@pytest.mark.parametrize("N", [8, 20, 64, 256])
+def test_router_gradients(N):
+    _backward(4097, N, 1024, "bf16", "none", out_f32=True, grad_f32=True)
+
+
+def test_backward_large():
+    _backward(3000, 1536, 1024, "bf16", "gelu")
+    _backward(2048, 2816, 1024, "bf16", "none")
+
+
+def test_gradients_against_differences():
+    """Central differences of a scalar of the forward pass (fp32): the step 2^-6 leaves a third-derivative term
+    below 2^-12 |dy| and a rounding term of 2 K u |z| / 2^-6."""
+    g = _gen(9)
+    M, N, K, e = 5, 6, 7, 2.0 ** -6
+    x, w, b = _mat(g, M, K, torch.float32), _mat(g, N, K, torch.float32, 0.4), torch.randn(N, device="cuda", generator=g)
+    dy = _mat(g, M, N, torch.float32)
+    for act in ("silu", "gelu"):
+        desc = moe.make_linear_desc(M, N, K, "f32", act)
+        z = torch.empty((M, N), device="cuda")
+        moe.Linear(desc, w, b).forward(x, z=z)
+        dx, dw, db = moe.Linear(desc, w, b).backward(x, dy, z=z)
+
+        def f(x_, w_, b_):
+            return float((moe.Linear(desc, w_, b_).forward(x_).double() * dy.double()).sum())
+
+        tol = float(dy.abs().sum()) * (2.0 ** -12 + 2.0 ** -12)
+        for grad, arg, make in ((dx, x, lambda t: (t, w, b)), (dw, w, lambda t: (x, t, b)), (db, b, lambda t: (x, w, t))):
+            for i in (0, arg.numel() // 2, arg.numel() - 1):
+                hi, lo = arg.clone(), arg.clone()
+                hi.view(-1)[i] += e
+                lo.view(-1)[i] -= e
+                assert abs((f(*make(hi)) - f(*make(lo))) / (2 * e) - float(grad.reshape(-1)[i])) <= tol
+
+
+def test_each_gradient_alone_equals_all_together():
+    g = _gen(11)
+    x, w, dy, z = (_mat(g, 300, 256, torch.bfloat16), _mat(g, 136, 256, torch.bfloat16), _mat(g, 300, 136, torch.bfloat16),
+                   _mat(g, 300, 136, torch.bfloat16))
+    layer = moe.Linear(moe.make_linear_desc(300, 136, 256, act="gelu"), w)
+    dx, dw, db = layer.backward(x, dy, z=z, need_db=True)
+    again = layer.backward(x, dy, z=z, need_db=True)
+    assert all(torch.equal(a, b) for a, b in zip((dx, dw, db), again))        # equal inputs, equal bits
+    assert torch.equal(layer.backward(x, dy, z=z, need_dw=False)[0], dx)
+    assert torch.equal(layer.backward(x, dy, z=z, need_dx=False)[1], dw)
+    only = layer.backward(x, dy, z=z, need_dx=False, need_dw=False, need_db=True)
+    assert only[0] is None and only[1] is None and torch.equal(only[2], db)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_rows(dtype):
+    dt = DT[dtype]
+    w = torch.ones((24, 64), device="cuda", dtype=dt)
+    layer = moe.Linear(moe.make_linear_desc(0, 24, 64, dtype), w)
+    x, dy = torch.empty((0, 64), device="cuda", dtype=dt), torch.empty((0, 24), device="cuda", dtype=dt)
+    assert layer.forward(x).shape == (0, 24)
+    dx, dw, db = layer.backward(x, dy, need_db=True)
+    assert dx.shape == (0, 64) and not dw.any() and not db.any()
+
+
+def test_side_stream_and_graph_replay():
+    g = _gen(12)
+    x, w, z = _mat(g, 129, 264, torch.bfloat16), _mat(g, 250, 264, torch.bfloat16, 0.1), None
+    layer = moe.Linear(moe.make_linear_desc(129, 250, 264, act="none"), w, torch.zeros(250, device="cuda"))
+    dy = _mat(g, 129, 250, torch.bfloat16)
+    want = (layer.forward(x), *layer.backward(x, dy))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = (layer.forward(x, stream=side), *layer.backward(x, dy, stream=side))
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = (layer.forward(x), *layer.backward(x, dy))
+    x2 = _mat(_gen(13), 129, 264, torch.bfloat16)
+    fresh = (layer.forward(x2), *layer.backward(x2, dy))
+    x.copy_(x2)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(fresh, out))
+
+
+def test_misaligned_bases_and_short_workspaces_are_refused():
+    w = torch.ones((32, 64), device="cuda", dtype=torch.bfloat16)
+    x = torch.ones((9, 64 + 8), device="cuda", dtype=torch.bfloat16)
+    layer = moe.Linear(moe.make_linear_desc(9, 32, 64), w)
+    with pytest.raises(moe.MoEError) as e:
+        layer.forward(x[:, 1:65])
+    assert e.value.status == moe.MOE_ERR_INVALID_ARG
+    desc = moe.make_linear_desc(9, 32, 64, act="silu")
+    dy = torch.ones((9, 32), device="cuda", dtype=torch.bfloat16)
+    ws = torch.empty(moe.moe_linear_backward_workspace_size(desc) - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(moe.MoEError) as e:
+        moe.moe_linear_backward(desc, x[:, :64], w, dy, dy, None, w.clone(), None, ws)
+    assert e.value.status == moe.MOE_ERR_WORKSPACE

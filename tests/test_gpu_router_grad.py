@@ -1,0 +1,444 @@
+"""The router's training operators (moe_balance_loss, moe_route_backward,
+moe_combine_backward) against their formulas in 64 bits, and a run of them
+together with the layer and the dense product.
+
+Tolerances.  The fast exponential of x is off by 2 + 1.17 |x| steps of fp32, so
+with logits within R of their row's maximum a probability is off by at most
+(2 (2 + 1.17 R) + E / 8 + 8) 2^-23 relative (numerator, denominator, their sum
+over at most 8 per lane and 5 shuffles, the quotient); that is `rp` below.  The
+log-sum-exp is off by 2^-20 + rp + |lse| 2^-23.  Sums over tokens add 2^-23 per
+addition in a chain of at most T / 8 + 64 terms, all of one sign.  A dot product
+of d terms in fp32 is off by at most d 2^-23 sum |a b|.  A rounding to bf16 is
+off by at most 2^-8 of the value.
+"""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import mixture_experts_layer_swiglu_b200 as moe
+
+S, H = 2.0 ** -23, torch.finfo(torch.bfloat16).eps / 2
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    moe.moe_get_device_status(reset=True)
+    yield
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status(reset=True) == moe.MOE_OK
+
+
+def _desc(T, E, k, d=64, zc=(0, 0, 0), shared=0, dtype="bf16", out_f32=False):
+    return moe.make_desc(T=T, d_model=d, top_k=k, dtype=dtype, n_ffn=E - sum(zc), hidden=128, n_zero=zc[0], n_copy=zc[1],
+                         n_const=zc[2], n_shared=shared, hidden_shared=128 if shared else 0, out_f32=out_f32)
+
+
+def _routed(T, E, k, seed=0, std=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.randn((T, E), device="cuda", generator=g) * std
+    top, idx = torch.sort(z, dim=1, descending=True, stable=True)
+    gate = torch.softmax(top[:, :k], dim=1).contiguous()
+    dgate = torch.randn((T, k), device="cuda", generator=g)
+    return z, idx[:, :k].to(torch.int32).contiguous(), gate, dgate
+
+
+def _reference(z, idx, k, mask, weight):
+    T, E = z.shape
+    z64 = z.double()
+    live = torch.ones(T, dtype=torch.bool, device="cuda") if mask is None else mask.bool()
+    n = int(live.sum())
+    dead_row = (z64 == -float("inf")).all(dim=1)
+    p = torch.softmax(z64, dim=1).masked_fill(dead_row[:, None], 0.0)
+    lse = torch.logsumexp(z64, dim=1).masked_fill(dead_row, 0.0)
+    counts = torch.bincount(idx[live].reshape(-1).long(), minlength=E)
+    w = torch.ones(E, dtype=torch.float64, device="cuda") if weight is None else weight.double()
+    wf = w * counts / max(n * k, 1)
+    pm = p[live].sum(0) / max(n, 1)
+    return p, lse, counts, n, wf, pm, torch.stack([E * (wf * pm).sum(), (lse[live] ** 2).sum() / max(n, 1)]), live
+
+
+def _rp(z):
+    fin = torch.where(z.isfinite(), z, 0.0)
+    R = float((fin.amax(1) - fin.amin(1)).max()) if z.numel() else 0.0
+    return (2 * (2 + 1.17 * R) + z.shape[1] / 8 + 8) * S
+
+
+def _check_loss(z, idx, gate, dgate, k, mask=None, weight=None, seed=0):
+    T, E = z.shape
+    desc = _desc(T, E, k)
+    b = moe.RouterGradBuffers(desc)
+    for t in (b.counts, b.prob_mean, b.losses, b.dlogits):
+        t.fill_(77)
+    b.workspace.fill_(255)                             # the scratch needs no clearing
+    moe.moe_balance_loss(desc, z, idx, mask, weight, b.counts, b.prob_mean, b.losses, b.workspace)
+    p, lse, counts, n, wf, pm, losses, live = _reference(z, idx, k, mask, weight)
+    assert b.counts.tolist() == counts.tolist() + [n]
+    rp, chain = _rp(z), (T / 8 + 64) * S
+    assert ((b.prob_mean.double() - pm).abs() <= (rp + chain) * pm + 1e-37).all()
+    assert abs(float(b.losses[0]) - float(losses[0])) <= (rp + chain + 8 * S) * float(losses[0])
+    el = 2.0 ** -20 + rp + lse.abs() * S
+    ez = float((2 * lse.abs() * el + el * el)[live].sum()) / max(n, 1) + (chain + 4 * S) * float(losses[1])
+    assert abs(float(b.losses[1]) - float(losses[1])) <= ez + 1e-37
+    dl = torch.tensor([0.3, 0.07], device="cuda")
+    cb, cz = float(dl[0].double()) * E / max(n, 1), 2 * float(dl[1].double()) / max(n, 1)
+    dot = (p @ wf)[:, None]
+    loss_part = (p * (cb * (wf - dot) + cz * lse[:, None])).masked_fill(~live[:, None], 0.0)
+    size = p * (cb * (wf + dot) * (2 * rp + 8 * S) + cz * (lse.abs() * (rp + 4 * S) + el)[:, None]) + 1e-37
+    gd, dd = gate.double(), dgate.double()
+    mean = (gd * dd).sum(1, keepdim=True)
+    gate_part = torch.zeros_like(p).scatter_add_(1, idx.long(), gd * (dd - mean))
+    gate_size = torch.zeros_like(p).scatter_add_(1, idx.long(), gd * (dd.abs() + (gd * dd).abs().sum(1, keepdim=True)) * 12 * S)
+    for dg, use in ((dgate, True), (None, False)):
+        for dls, losses_too in ((dl, True), (None, False)):
+            if dg is None and dls is None:
+                continue
+            b.dlogits.fill_(77)
+            moe.moe_route_backward(desc, z, idx, gate, dg, mask, weight, b.counts, dls, b.dlogits)
+            want = gate_part * use + loss_part * losses_too
+            tol = gate_size * use + size * losses_too + 2 * S * want.abs()
+            assert ((b.dlogits.double() - want).abs() <= tol + 1e-37).all()
+    return b
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (2, 3, 3), (31, 8, 2), (64, 8, 2), (129, 16, 4), (257, 17, 1),
+                                   (1000, 20, 2), (333, 33, 6), (2048, 64, 6), (515, 100, 32), (4096, 128, 8),
+                                   (9001, 256, 8), (40000, 8, 2)])
+def test_balance_loss_and_its_gradient(T, E, k):
+    _check_loss(*_routed(T, E, k, seed=T), k)
+
+
+@pytest.mark.parametrize("T,E,k", [(70, 8, 2), (5000, 20, 2), (3000, 200, 8)])
+def test_padded_batches_and_expert_weights(T, E, k):
+    z, idx, gate, dgate = _routed(T, E, k)
+    mask = (torch.arange(T, device="cuda") % 3 != 0).to(torch.uint8)
+    weight = torch.linspace(0.0, 2.0, E, device="cuda")
+    z[::3] = float("nan")                              # a padding row's logits must not matter to the losses
+    desc = _desc(T, E, k)
+    b = moe.RouterGradBuffers(desc)
+    moe.moe_balance_loss(desc, z, idx, mask, weight, b.counts, b.prob_mean, b.losses, b.workspace)
+    assert b.losses.isfinite().all()
+    dl = torch.ones(2, device="cuda")
+    moe.moe_route_backward(desc, z, idx, gate, None, mask, weight, b.counts, dl, b.dlogits)
+    assert b.dlogits.isfinite().all() and not b.dlogits[::3].any()
+    z[::3] = 0.5
+    _check_loss(z, idx, gate, dgate, k, mask, weight)
+    _check_loss(z, idx, gate, dgate, k, mask.bool(), None)
+
+
+def test_no_counted_token_and_no_token():
+    z, idx, gate, dgate = _routed(40, 8, 2)
+    b = _check_loss(z, idx, gate, dgate, 2, torch.zeros(40, dtype=torch.uint8, device="cuda"))
+    assert not b.losses.any() and not b.counts.any() and not b.prob_mean.any()
+    desc = _desc(0, 8, 2)
+    b = moe.RouterGradBuffers(desc)
+    for t in (b.counts, b.prob_mean, b.losses):
+        t.fill_(5)
+    e = torch.empty((0, 8), device="cuda")
+    i = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    moe.moe_balance_loss(desc, e, i, None, None, b.counts, b.prob_mean, b.losses, b.workspace)
+    assert not b.losses.any() and not b.counts.any() and not b.prob_mean.any()
+    moe.moe_route_backward(desc, e, i, None, None, None, None, b.counts, b.losses, b.dlogits)
+
+
+def test_masked_out_experts_and_rows():
+    """Logits of -inf (an expert switched off) and rows of nothing else; the lowest finite value."""
+    z, idx, gate, dgate = _routed(300, 40, 4)
+    z[:, 7] = -float("inf")
+    z[:, 11] = torch.finfo(torch.float32).min
+    z[5] = -float("inf")
+    z[6] = torch.finfo(torch.float32).min
+    idx = torch.sort(z, dim=1, descending=True, stable=True)[1][:, :4].to(torch.int32).contiguous()
+    p, lse, counts, n, wf, pm, losses, live = _reference(z, idx, 4, None, None)
+    desc = _desc(300, 40, 4)
+    b = moe.RouterGradBuffers(desc)
+    moe.moe_balance_loss(desc, z, idx, None, None, b.counts, b.prob_mean, b.losses, b.workspace)
+    assert b.counts.tolist() == counts.tolist() + [300]
+    assert ((b.prob_mean.double() - pm).abs() <= 1e-5 * pm + 1e-37).all()
+    # (row 6 gives all 40 experts, the switched-off one too, the same logit: 1 / 40 each)
+    assert abs(float(b.prob_mean[7]) - 1 / 40 / 300) <= 1e-5 / 40 / 300
+    dl = torch.tensor([1.0, 0.0], device="cuda")
+    moe.moe_route_backward(desc, z, idx, gate, None, None, None, b.counts, dl, b.dlogits)
+    others = torch.arange(300, device="cuda") != 6
+    assert not b.dlogits[5].any() and not b.dlogits[others, 7].any()
+    assert b.dlogits.isfinite().all()
+
+
+def test_nan_logits_show():
+    z, idx, gate, dgate = _routed(64, 20, 2)
+    z[9, 3] = float("nan")
+    desc = _desc(64, 20, 2)
+    b = moe.RouterGradBuffers(desc)
+    moe.moe_balance_loss(desc, z, idx, None, None, b.counts, b.prob_mean, b.losses, b.workspace)
+    assert b.losses.isnan().all()
+    moe.moe_route_backward(desc, z, idx, gate, dgate, None, None, b.counts, torch.ones(2, device="cuda"), b.dlogits)
+    assert b.dlogits[9].isnan().all() and b.dlogits[torch.arange(64, device="cuda") != 9].isfinite().all()
+
+
+def test_ids_out_of_range_and_the_same_id_twice():
+    z, idx, gate, dgate = _routed(50, 8, 3)
+    idx[4] = torch.tensor([2, 2, 2], dtype=torch.int32)
+    desc = _desc(50, 8, 3)
+    _check_loss(z, idx, gate, dgate, 3)
+    idx[7, 1], idx[9, 0] = 8, -1
+    b = moe.RouterGradBuffers(desc)
+    moe.moe_balance_loss(desc, z, idx, None, None, b.counts, b.prob_mean, b.losses, b.workspace)
+    torch.cuda.synchronize()
+    assert int(b.counts[:8].sum()) == 50 * 3 - 2
+    assert moe.moe_get_device_status(reset=True) == moe.MOE_ERR_DEVICE_BOUNDS
+    moe.moe_route_backward(desc, z, idx, gate, dgate, None, None, b.counts, None, b.dlogits)
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status(reset=True) == moe.MOE_ERR_DEVICE_BOUNDS
+
+
+def test_gradient_against_differences():
+    """The losses' gradient with the counts held fixed: a step of 1/64 in one logit of a batch of 4 tokens moves the
+    two losses by what dlogits says, up to the third-order term (below 1e-4 here) and the rounding of the losses
+    (3e-6 / (1/32))."""
+    z, idx, gate, _ = _routed(4, 6, 2, std=1.0)
+    desc = _desc(4, 6, 2)
+    b = moe.RouterGradBuffers(desc)
+    dl = torch.tensor([1.0, 0.25], device="cuda")
+
+    def total(zz):
+        moe.moe_balance_loss(desc, zz, idx, None, None, b.counts, b.prob_mean, b.losses, b.workspace)
+        return float(b.losses.double() @ dl.double())
+
+    total(z)
+    moe.moe_route_backward(desc, z, idx, gate, None, None, None, b.counts, dl, b.dlogits)
+    for t, e in ((0, 0), (1, 5), (3, 2)):
+        hi, lo = z.clone(), z.clone()
+        hi[t, e] += 1 / 64
+        lo[t, e] -= 1 / 64
+        assert abs((total(hi) - total(lo)) * 32 - float(b.dlogits[t, e])) <= 2e-4 + 2e-4
+
+
+def test_logits_gradient_in_place():
+    z, idx, gate, dgate = _routed(700, 64, 6)
+    desc = _desc(700, 64, 6)
+    b = moe.RouterGradBuffers(desc)
+    moe.moe_balance_loss(desc, z, idx, None, None, b.counts, b.prob_mean, b.losses, b.workspace)
+    dl = torch.ones(2, device="cuda")
+    moe.moe_route_backward(desc, z, idx, gate, dgate, None, None, b.counts, dl, b.dlogits)
+    moe.moe_route_backward(desc, z, idx, gate, dgate, None, None, b.counts, dl, z)
+    assert torch.equal(z, b.dlogits)
+
+
+# ------------------------------------------------------------ combine
+
+def _combine_case(T, E, k, d, zc, shared, dtype, out_f32, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    desc = _desc(T, E, k, d, zc, shared, dtype, out_f32)
+    n_ffn, n_const = desc.n_ffn, desc.n_const
+    idx = torch.rand((T, E), device="cuda", generator=g).argsort(dim=1)[:, :k].to(torch.int32).contiguous()
+    gate = torch.softmax(torch.randn((T, k), device="cuda", generator=g), dim=1)
+    cap = moe.moe_row_capacity(desc)
+    off = torch.empty(n_ffn + shared + 1, dtype=torch.int32, device="cuda")
+    row_of = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    tok = torch.empty(cap, dtype=torch.int32, device="cuda")
+    x = torch.randn((T, d), device="cuda", generator=g).to(dt)
+    ws = torch.empty(moe.moe_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    moe.moe_permute(desc, idx, x, off, row_of, tok, torch.empty((cap, d), dtype=dt, device="cuda"), ws)
+    ys = torch.randn((cap, d), device="cuda", generator=g)
+    dy = torch.randn((T, d), device="cuda", generator=g).to(torch.float32 if out_f32 else dt)
+    mix = torch.softmax(torch.randn((T, n_const, 2), device="cuda", generator=g), dim=-1)
+    vec = torch.randn((n_const, d), device="cuda", generator=g).to(dt)
+    return desc, idx, gate, off, row_of, x, ys, dy, mix, vec, dt
+
+
+def _check_combine(T, E, k, d, zc=(0, 0, 0), shared=0, dtype="bf16", out_f32=False, seed=0):
+    desc, idx, gate, off, row_of, x, ys, dy, mix, vec, dt = _combine_case(T, E, k, d, zc, shared, dtype, out_f32, seed)
+    n_ffn, n_const = desc.n_ffn, desc.n_const
+    copy0, const0 = n_ffn + zc[0], n_ffn + zc[0] + zc[1]
+    cap = ys.shape[0]
+    f32 = dict(dtype=torch.float32, device="cuda")
+    dgate = torch.full((T, k), 77.0, **f32)
+    dys = torch.full((cap, d), 77.0, dtype=dt, device="cuda")
+    dx = torch.full((T, d), 77.0, dtype=dt, device="cuda")
+    dmix = torch.full((T, n_const, 2), 77.0, **f32) if n_const else None
+    dvec = torch.full((n_const, d), 77.0, **f32) if n_const else None
+    moe.moe_combine_backward(desc, {"const_vec": vec}, dy, ys, off, row_of, idx, gate, mix, x, dgate, dys, dx, dmix, dvec)
+    D, X, G = dy.double(), x.double(), gate.double()
+    rnd = H if dt == torch.bfloat16 else S / 2
+    written = torch.zeros(cap, dtype=torch.bool, device="cuda")
+    coef = torch.zeros(T, dtype=torch.float64, device="cuda")
+    want_mix = torch.zeros((T, n_const, 2), dtype=torch.float64, device="cuda")
+    mix_tol = torch.zeros_like(want_mix)
+    want_vec = torch.zeros((n_const, d), dtype=torch.float64, device="cuda")
+    vec_mag = torch.zeros_like(want_vec)
+    xdot, xmag = (X * D).sum(1), (X * D).abs().sum(1)
+    for j in range(k):
+        e, r = idx[:, j].long(), row_of[:, j].long()
+        at = torch.nonzero(e < n_ffn).reshape(-1)
+        O = ys[r[at]].double()
+        err = (dgate[at, j].double() - (O * D[at]).sum(1)).abs()
+        assert (err <= d * S * (O * D[at]).abs().sum(1) + 1e-37).all()
+        want = G[at, j, None] * D[at]
+        assert ((dys[r[at]].double() - want).abs() <= (rnd + S) * want.abs() + 1e-37).all()
+        written[r[at]] = True
+        zero = (e >= n_ffn) & (e < copy0)
+        assert not dgate[zero, j].any()
+        cp = (e >= copy0) & (e < const0)
+        assert ((dgate[cp, j].double() - xdot[cp]).abs() <= d * S * xmag[cp] + 1e-37).all()
+        coef += torch.where(cp, G[:, j], 0.0)
+        for c in range(n_const):
+            at = torch.nonzero(e == const0 + c).reshape(-1)
+            a, v = mix[at, c].double(), vec[c].double()
+            vdot, vmag = (D[at] * v).sum(1), (D[at] * v).abs().sum(1)
+            tol = (d + 4) * S * (a[:, 0] * xmag[at] + a[:, 1] * vmag)
+            assert ((dgate[at, j].double() - a[:, 0] * xdot[at] - a[:, 1] * vdot).abs() <= tol + 1e-37).all()
+            coef[at] += G[at, j] * a[:, 0]
+            g = G[at, j]
+            want_mix[at, c] += torch.stack([g * xdot[at], g * vdot], 1)
+            mix_tol[at, c] += torch.stack([g * xmag[at], g * vmag], 1) * (d + 4) * S
+            want_vec[c] += ((g * a[:, 1])[:, None] * D[at]).sum(0)
+            vec_mag[c] += ((g * a[:, 1])[:, None] * D[at]).abs().sum(0)
+    assert ((dx.double() - coef[:, None] * D).abs() <= (rnd + (k + 3) * S) * (coef[:, None] * D).abs() + 1e-37).all()
+    if n_const:
+        assert ((dmix.double() - want_mix).abs() <= mix_tol + 1e-37).all()
+        assert ((dvec.double() - want_vec).abs() <= (T * k / 8 + 16) * S * vec_mag + 1e-37).all()
+    for s in range(shared):
+        lo = int(off[n_ffn + s])
+        assert ((dys[lo:lo + T].double() - D).abs() <= rnd * D.abs()).all()
+        written[lo:lo + T] = True
+    assert (dys[~written] == 77.0).all()               # rows of no slot stay as they were
+
+
+@pytest.mark.parametrize("T,E,k,d,zc,shared", [
+    (1, 2, 1, 64, (0, 0, 0), 0), (5, 8, 2, 256, (0, 0, 0), 0), (333, 20, 2, 2048, (1, 1, 2), 0), (100, 16, 6, 448, (0, 0, 0), 2),
+    (257, 12, 5, 4160, (2, 2, 3), 1), (64, 40, 32, 128, (1, 1, 1), 0), (300, 4, 2, 512, (1, 1, 1), 0), (128, 3, 3, 64, (1, 1, 1), 0),
+    (2000, 64, 6, 1024, (0, 0, 0), 2)])
+def test_combine_backward(T, E, k, d, zc, shared):
+    _check_combine(T, E, k, d, zc, shared)
+
+
+@pytest.mark.parametrize("dtype,out_f32", [("bf16", True), ("f32", False)])
+def test_combine_backward_types(dtype, out_f32):
+    _check_combine(130, 14, 3, 264 if dtype == "f32" else 320, (1, 1, 2), 1, dtype, out_f32)
+
+
+def test_combine_backward_layer_of_zero_computation_experts_only():
+    _check_combine(90, 6, 2, 128, (2, 2, 2), 0)
+
+
+def test_combine_backward_outputs_one_by_one():
+    desc, idx, gate, off, row_of, x, ys, dy, mix, vec, dt = _combine_case(200, 14, 3, 512, (1, 1, 2), 1, "bf16", False)
+    cap = ys.shape[0]
+
+    def fresh():
+        f32 = dict(dtype=torch.float32, device="cuda")
+        return [torch.zeros((200, 3), **f32), torch.zeros((cap, 512), dtype=dt, device="cuda"),
+                torch.zeros((200, 512), dtype=dt, device="cuda"), torch.zeros((200, 2, 2), **f32), torch.zeros((2, 512), **f32)]
+
+    def call(out, **none):
+        a = dict(ys=ys, off=off, mix=mix, x=x, w={"const_vec": vec})
+        a.update(none)
+        moe.moe_combine_backward(desc, a["w"], dy, a["ys"], a["off"], row_of, idx, gate, a["mix"], a["x"], *out)
+
+    every = fresh()
+    call(every)
+    needs_not = [dict(off=None), dict(ys=None, mix=None, x=None, w={}), dict(ys=None, off=None, x=None, w={}),
+                 dict(ys=None, off=None), dict(ys=None, off=None, x=None, w={})]
+    for i in range(5):
+        out, one = fresh(), [None] * 5
+        one[i] = out[i]
+        call(one, **needs_not[i])
+        assert torch.equal(out[i], every[i]), i
+
+
+def test_combine_backward_bad_rows_and_ids():
+    desc, idx, gate, off, row_of, x, ys, dy, mix, vec, dt = _combine_case(60, 8, 2, 128, (0, 0, 0), 0, "bf16", False)
+    idx[3, 0], row_of[4, 1], row_of[5, 0] = 99, ys.shape[0], -1
+    dgate = torch.full((60, 2), 77.0, device="cuda")
+    dys = torch.zeros((ys.shape[0], 128), dtype=dt, device="cuda")
+    moe.moe_combine_backward(desc, {}, dy, ys, off, row_of, idx, gate, None, None, dgate, dys, None, None, None)
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status(reset=True) == moe.MOE_ERR_DEVICE_BOUNDS
+    assert float(dgate[3, 0]) == 0 and float(dgate[4, 1]) == 0 and float(dgate[5, 0]) == 0
+    assert dgate.isfinite().all()
+
+
+# ------------------------------------------------------------ together
+
+def test_router_training_step_end_to_end():
+    """A router-tuning step of a small layer with frozen experts: the forward pass by the layer's stages, the two
+    losses, and the gradients of the router's weights, bias, input and previous logits, against torch's autograd in
+    64 bits on the same selection.  The expert outputs y_sorted are taken as the GPU gave them (constants), so what is
+    compared are the gradients' own steps; the weights' gradient passes one bf16 rounding of x W (none: dw is fp32 and
+    takes dlogits in 24 bits), its bound 1e-4 of the largest entry covers the probabilities' (rp) and sums' errors."""
+    from moe_workloads import get_config, make_inputs, scaled
+    cfg = scaled(get_config("moepp"), T=150, d=256, hidden=256)
+    inp = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in make_inputs(cfg).items()}
+    desc = moe.desc_from(cfg, out_f32=True)
+    T, d, E, k = cfg.T, cfg.d, cfg.n_routed, cfg.top_k
+    bufs, rb = moe.StageBuffers(desc), moe.RouterGradBuffers(desc)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randn((T, d), device="cuda", generator=g)
+    coef = torch.tensor([0.5, 0.01], device="cuda")
+    moe.run_stages(desc, inp, inp["x"], bufs, prev_logits=inp["z_prev"])
+    moe.moe_balance_loss(desc, bufs.logits, bufs.idx, None, None, rb.counts, rb.prob_mean, rb.losses, rb.workspace)
+    moe.moe_combine_backward(desc, inp, dy, bufs.y_sorted, bufs.offsets, bufs.row_of, bufs.idx, bufs.gate, bufs.const_mix,
+                             inp["x"], rb.dgate, None, None, None, None)
+    moe.moe_route_backward(desc, bufs.logits, bufs.idx, bufs.gate, rb.dgate, None, None, rb.counts, coef, rb.dlogits)
+    router = moe.Linear(moe.make_linear_desc(T, E, d, out_f32=True, grad_f32=True), inp["w_router"], inp["router_bias"])
+    dx, dw, db = router.backward(inp["x"], rb.dlogits)
+    # the router's logits are the dense product with bias and residual
+    z = router.forward(inp["x"], residual=inp["z_prev"])
+    assert ((z - bufs.logits).abs() <= 1e-5 * (1 + bufs.logits.abs())).all()
+
+    W, B = inp["w_router"].double().requires_grad_(), inp["router_bias"].double().requires_grad_()
+    X, Zp = inp["x"].double().requires_grad_(), inp["z_prev"].double().requires_grad_()
+    z64 = X @ W.T + B + Zp
+    idx = bufs.idx.long()
+    gate = torch.softmax(z64.gather(1, idx), dim=1)
+    O = torch.zeros((T, k, d), dtype=torch.float64, device="cuda")
+    x0, n_ffn = inp["x"].double(), cfg.n_ffn
+    for t in range(T):
+        for j in range(k):
+            e = int(idx[t, j])
+            if e < n_ffn:
+                O[t, j] = bufs.y_sorted[int(bufs.row_of[t, j])].double()
+            elif e == n_ffn + 1:
+                O[t, j] = x0[t]
+            elif e >= n_ffn + 2:
+                c = e - n_ffn - 2
+                a = bufs.const_mix[t, c].double()
+                O[t, j] = a[0] * x0[t] + a[1] * inp["const_vec"][c].double()
+    y = (gate[:, :, None] * O).sum(1)
+    p = torch.softmax(z64, dim=1)
+    f = torch.bincount(idx.reshape(-1), minlength=E).double() / (T * k)
+    loss = (y * dy.double()).sum() + 0.5 * E * (f * p.mean(0)).sum() + 0.01 * (torch.logsumexp(z64, 1) ** 2).mean()
+    loss.backward()
+    for name, got, want, tol in (("dw", dw, W.grad, 1e-4), ("db", db, B.grad, 1e-4), ("dlogits", rb.dlogits, Zp.grad, 1e-4),
+                                 ("dx", dx, X.grad, 4 * H)):
+        assert float((got.double() - want).abs().max()) <= tol * float(want.abs().max()), name
+
+
+def test_training_step_replayed_from_a_graph():
+    z, idx, gate, dgate = _routed(3000, 64, 6)
+    desc = _desc(3000, 64, 6)
+    b = moe.RouterGradBuffers(desc)
+    dl = torch.ones(2, device="cuda")
+
+    def step():
+        moe.moe_balance_loss(desc, z, idx, None, None, b.counts, b.prob_mean, b.losses, b.workspace)
+        moe.moe_route_backward(desc, z, idx, gate, dgate, None, None, b.counts, dl, b.dlogits)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    z2, idx2, gate2, dgate2 = _routed(3000, 64, 6, seed=8)
+    for a, c in ((z, z2), (idx, idx2), (gate, gate2), (dgate, dgate2)):
+        a.copy_(c)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (b.counts, b.prob_mean, b.losses, b.dlogits)]
+    for t in (b.counts, b.prob_mean, b.losses, b.dlogits):
+        t.fill_(3)
+    step()
+    assert all(torch.equal(p, q) for p, q in zip(got, (b.counts, b.prob_mean, b.losses, b.dlogits)))

@@ -1,0 +1,136 @@
+"""The training entry points on a machine without a GPU: sizes, refusals of
+descriptors and arguments, and the shape checks of the objects above them."""
+
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+from mixture_experts_layer_swiglu_b200 import _abi as abi
+from mixture_experts_layer_swiglu_b200 import layer as L
+from mixture_experts_layer_swiglu_b200.linear import Linear, make_linear_desc
+
+P = 1 << 20            # an aligned address: only checks that run before any launch may see it
+
+
+def _lin(**kw):
+    return make_linear_desc(**{**dict(M=8, N=24, K=64), **kw})
+
+
+@pytest.mark.parametrize("bad", [dict(M=-1), dict(N=0), dict(K=0), dict(ld_x=63), dict(ld_w=1), dict(ld_y=23), dict(ld_r=-5),
+                                 dict(ld_z=23), dict(ld_dx=63)])
+def test_linear_descriptors_refused(bad):
+    d = _lin(**bad)
+    assert abi.moe_linear_workspace_size(d) == -1 and abi.moe_linear_backward_workspace_size(d) == -1
+    assert abi.load().moe_linear(ctypes.byref(d), P, P, None, None, P, None, None, 0, None) == abi.MOE_ERR_INVALID_ARG
+    assert abi.load().moe_linear_backward(ctypes.byref(d), P, P, P, P, P, P, None, P, 1 << 40,
+                                          None) == abi.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("field,value", [("dtype", 2), ("act", 4), ("act", -1), ("out_f32", 2), ("grad_f32", -1)])
+def test_linear_codes_refused(field, value):
+    d = _lin()
+    setattr(d, field, value)
+    assert abi.moe_linear_workspace_size(d) == -1 and abi.moe_linear_backward_workspace_size(d) == -1
+
+
+def test_linear_arguments_refused():
+    lib, d = abi.load(), _lin(act="gelu")
+    r = ctypes.byref(d)
+    bad = abi.MOE_ERR_INVALID_ARG
+    assert lib.moe_linear(None, P, P, None, None, P, None, None, 0, None) == bad
+    for x, w, y in ((None, P, P), (P, None, P), (P, P, None), (P + 2, P, P), (P, P + 8, P), (P, P, P + 4)):
+        assert lib.moe_linear(r, x, w, None, None, y, None, None, 0, None) == bad
+    assert lib.moe_linear(r, P, P, P + 2, None, P, None, None, 0, None) == bad           # bias
+    both = _lin(ld_r=32)
+    assert lib.moe_linear(ctypes.byref(both), P, P, None, P, P, None, None, 0, None) == bad   # y in residual, other strides
+    big = 1 << 40
+    for x, w, z, dy, dx, dw, db in ((P, P, P, P, None, None, None), (None, P, P, P, P, P, None), (P, None, P, P, P, P, None),
+                                    (P, P, None, P, P, P, None), (P, P, P, None, P, P, None), (P, P, P, P + 2, P, P, None),
+                                    (P, P, P, P, P, P, P + 1)):
+        assert lib.moe_linear_backward(r, x, w, z, dy, dx, dw, db, P, big, None) == bad
+    assert lib.moe_linear_backward(r, P, P, P, P, P, P, P, None, 0, None) == abi.MOE_ERR_WORKSPACE
+    assert lib.moe_last_launch_count() == 0
+
+
+def test_linear_object_refuses_what_disagrees_with_it():
+    bf, f32 = torch.bfloat16, torch.float32
+    w = torch.zeros(24, 64, dtype=bf)
+    lay = Linear(_lin(act="silu"), w, torch.zeros(24))
+    x, dy, z = torch.zeros(5, 64, dtype=bf), torch.zeros(5, 24, dtype=bf), torch.zeros(5, 24, dtype=bf)
+    bad = [lambda: Linear(_lin(), torch.zeros(24, 63, dtype=bf)), lambda: Linear(_lin(), w.float()),
+           lambda: Linear(_lin(), torch.zeros(24, 72, dtype=bf)[:, :64]), lambda: Linear(_lin(), w, torch.zeros(25)),
+           lambda: Linear(_lin(), w, torch.zeros(24, dtype=bf)),
+           lambda: lay.forward(x.float()), lambda: lay.forward(x[0]), lambda: lay.forward(x, residual=dy.float()),
+           lambda: lay.forward(x, y=torch.zeros(4, 24, dtype=bf)), lambda: lay.forward(x, z=torch.zeros(5, 24, dtype=f32)),
+           lambda: lay.forward(torch.zeros(64, 5, dtype=bf).t()),                        # columns contiguous
+           lambda: lay.forward(torch.zeros(1, 64, dtype=bf).expand(5, 64)),              # rows on top of one another
+           lambda: lay.backward(x, dy), lambda: lay.backward(x, dy.float(), z=z),
+           lambda: lay.backward(x, dy, z=z, dw=torch.zeros(24, 64)), lambda: lay.backward(x, dy, z=z, db=torch.zeros(23))]
+    for call in bad:
+        with pytest.raises(ValueError, match="expected|needs"):
+            call()
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        lay.forward(x)
+
+
+def _layer(**kw):
+    return L.make_desc(**{**dict(T=8, d_model=256, top_k=2, n_ffn=4, hidden=256), **kw})
+
+
+ATOMIC = dict(T=8, d_model=256, top_k=4, kind="atomic", pk_rows=32, pk_cols=32, pk_topk_half=4, d_query=64, n_ffn=0, hidden=0)
+
+
+def test_balance_loss_and_route_backward_refusals():
+    lib, d = abi.load(), _layer()
+    need = abi.moe_balance_loss_workspace_size(d)
+    assert need > 0
+    atomic = _layer(**ATOMIC)
+    assert abi.moe_balance_loss_workspace_size(atomic) == -1
+    assert abi.moe_balance_loss_workspace_size(_layer(top_k=5)) == -1
+    good = dict(logits=P, idx=P, mask=None, weight=None, counts=P, prob=P, losses=P, ws=P, n=need)
+
+    def loss(desc, **kw):
+        a = {**good, **kw}
+        return lib.moe_balance_loss(ctypes.byref(desc), a["logits"], a["idx"], a["mask"], a["weight"], a["counts"], a["prob"],
+                                    a["losses"], a["ws"], a["n"], None)
+
+    assert loss(atomic) == abi.MOE_ERR_UNSUPPORTED
+    for kw in (dict(logits=None), dict(idx=None), dict(counts=None), dict(prob=None), dict(losses=None), dict(logits=P + 4),
+               dict(weight=P + 2)):
+        assert loss(d, **kw) == abi.MOE_ERR_INVALID_ARG
+    for kw in (dict(ws=None), dict(n=need - 1), dict(ws=P + 8)):
+        assert loss(d, **kw) == abi.MOE_ERR_WORKSPACE
+
+    def back(desc, logits=P, idx=P, gate=P, dgate=P, counts=P, dl=P, out=P):
+        return lib.moe_route_backward(ctypes.byref(desc), logits, idx, gate, dgate, None, None, counts, dl, out, None)
+
+    assert back(atomic) == abi.MOE_ERR_UNSUPPORTED
+    for kw in (dict(dgate=None, dl=None), dict(logits=None), dict(idx=None), dict(gate=None), dict(counts=None), dict(out=None),
+               dict(out=P + 4), dict(dl=P + 2)):
+        assert back(d, **kw) == abi.MOE_ERR_INVALID_ARG
+    assert lib.moe_last_launch_count() == 0
+
+
+def test_combine_backward_refusals():
+    lib = abi.load()
+    d = _layer(n_zero=1, n_copy=1, n_const=1, n_shared=1, hidden_shared=256)
+    w = abi.MoELayerWeights()
+    w.const_vec = P
+    names = ("dy", "ys", "off", "row", "idx", "gate", "mix", "x", "dgate", "dys", "dx", "dmix", "dvec")
+
+    def call(desc, weights=w, **kw):
+        a = {**dict.fromkeys(names, P), **kw}
+        return lib.moe_combine_backward(ctypes.byref(desc), ctypes.byref(weights), *(a[n] for n in names), None)
+
+    assert call(_layer(**ATOMIC)) == abi.MOE_ERR_UNSUPPORTED
+    for kw in (dict(dy=None), dict(ys=None), dict(off=None), dict(row=None), dict(idx=None), dict(gate=None), dict(mix=None),
+               dict(x=None), dict(dy=P + 8), dict(dys=P + 2), dict(dgate=P + 1),
+               dict(dgate=None, dys=None, dx=None, dmix=None, dvec=None)):
+        assert call(d, **kw) == abi.MOE_ERR_INVALID_ARG, kw
+    assert call(d, weights=abi.MoELayerWeights()) == abi.MOE_ERR_INVALID_ARG
+    plain = _layer()
+    assert call(plain) == abi.MOE_ERR_INVALID_ARG                      # constant experts' gradients of a layer without any
+    assert lib.moe_last_launch_count() == 0
