@@ -1,5 +1,6 @@
 // linear.cu -- the dense product and its gradients: argument checks, the
-// workspace, the pass that forms dz and db, and the order of the products.
+// workspace, the pass that forms dz and db, the copies of rows that TMA cannot
+// address, and the order of the products.
 
 #include <algorithm>
 
@@ -48,12 +49,26 @@ constexpr int DZ_COLS = 128;
 struct DzArgs {
     const void* dy;
     const void* z;
-    float* dz;
+    void* dz;                    // fp32, or `parts` bf16 planes
     float* part;
-    long long ld_dy, ld_z, ld_dz;
+    long long ld_dy, ld_z, ld_dz, plane;
     int M, N, act, rows;         // rows per range
-    int dy_f32, z_f32;
+    int dy_f32, z_f32, dz_f32, parts;
 };
+
+// v as a sum of bf16 values: each part the nearest bf16 of what the parts
+// before it left (24 bits in three).  An infinity or NaN is its first part.
+__device__ __forceinline__ void store_parts(__nv_bfloat16* p, long long plane, int parts, float v)
+{
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    p[0] = hi;
+    if (parts == 1) return;
+    const float h = __bfloat162float(hi);
+    const float r1 = fabsf(h) < INFINITY ? v - h : 0.f;
+    const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
+    p[plane] = mid;
+    p[2 * plane] = __float2bfloat16_rn(r1 - __bfloat162float(mid));
+}
 
 __device__ __forceinline__ float ld1(const void* p, long long i, int f32)
 {
@@ -75,7 +90,10 @@ __global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
             float v = ld1(a.dy, (long long)m * a.ld_dy + c, a.dy_f32);
             if (a.act != MOE_ACT_NONE) v *= act_slope(ld1(a.z, (long long)m * a.ld_z + c, a.z_f32), a.act);
             acc[i] += v;
-            if (a.dz) a.dz[(long long)m * a.ld_dz + c] = v;
+            if (!a.dz) continue;
+            const long long at = (long long)m * a.ld_dz + c;
+            if (a.dz_f32) static_cast<float*>(a.dz)[at] = v;
+            else store_parts(static_cast<__nv_bfloat16*>(a.dz) + at, a.plane, a.parts, v);
         }
     }
     if (!a.part) return;
@@ -109,8 +127,41 @@ int dz_chunks(const Lin& l, int* rows)
     return cdiv(std::max(l.M, 1), *rows);
 }
 
-// dz needs a buffer of its own unless it is dy as it stands.
-bool dz_is_dy(const Lin& l) { return l.act == MOE_ACT_NONE && l.of32 == l.f32; }
+// ------------------------------------------------------------ packed rows
+// [rows, cols] bf16 to rows of ld_dst elements (a TMA tensor's row stride is a
+// multiple of 16 bytes).  What lies between cols and ld_dst is never read.
+__global__ void __launch_bounds__(256) linear_pack_kernel(const __nv_bfloat16* src, long long ld_src, int rows, int cols,
+                                                          __nv_bfloat16* dst, long long ld_dst)
+{
+    for (long long r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int c = threadIdx.x; c < cols; c += 256) dst[r * ld_dst + c] = src[r * ld_src + c];
+}
+
+inline long long up8(long long n) { return (n + 7) & ~7ll; }
+
+// The operand as TMA can read it: itself, or (ld not a multiple of 8) a copy.
+struct Rows {
+    const void* p;
+    long long ld;
+};
+size_t packed_bytes(bool f32, long long rows, long long cols, long long ld)
+{
+    return f32 || ld % 8 == 0 ? 0 : al((size_t)rows * up8(cols) * 2);
+}
+Rows packed(const void* p, int rows, int cols, long long ld, char*& ws, cudaStream_t st)
+{
+    if (ld % 8 == 0) return Rows{p, ld};
+    const Rows r{ws, up8(cols)};
+    linear_pack_kernel<<<std::min(rows, 8 * num_sms()), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(p), ld, rows, cols,
+                                                                       reinterpret_cast<__nv_bfloat16*>(ws), r.ld);
+    count_launch();
+    ws += al((size_t)rows * r.ld * 2);
+    return r;
+}
+
+// dz needs no buffer of its own where it is dy as it stands.
+bool dz_is_dy(const Lin& l) { return l.act == MOE_ACT_NONE && l.of32 == l.f32 && (l.f32 || l.ld_y % 8 == 0); }
+int dz_parts(const Lin& l) { return l.gf32 && !l.f32 && (l.act != MOE_ACT_NONE || l.of32) ? 3 : 1; }
 
 struct BwdLayout {
     size_t dz, part, total;
@@ -120,9 +171,9 @@ BwdLayout bwd_layout(const Lin& l)
 {
     BwdLayout b{0, 0, 0};
     int rows;
-    b.dz = dz_is_dy(l) ? 0 : al((size_t)l.M * l.N * 4);
+    b.dz = dz_is_dy(l) ? 0 : al(l.f32 ? (size_t)l.M * l.N * 4 : (size_t)dz_parts(l) * l.M * up8(l.N) * 2);
     b.part = al((size_t)dz_chunks(l, &rows) * l.N * 4);
-    b.total = b.dz + b.part;
+    b.total = b.dz + b.part + packed_bytes(l.f32, l.M, l.K, l.ld_x) + packed_bytes(l.f32, l.N, l.K, l.ld_w);
     return b;
 }
 
@@ -142,7 +193,7 @@ int64_t moe_linear_workspace_size(const moe_linear_desc* d)
 {
     Lin l;
     if (read_desc(d, l) != MOE_OK) return -1;
-    return 0;
+    return (int64_t)(packed_bytes(l.f32, l.M, l.K, l.ld_x) + packed_bytes(l.f32, l.N, l.K, l.ld_w));
 }
 
 int64_t moe_linear_backward_workspace_size(const moe_linear_desc* d)
@@ -166,18 +217,14 @@ moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* w, co
     const size_t need = (size_t)moe_linear_workspace_size(d);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace))) return MOE_ERR_WORKSPACE;
     if (l.M == 0) return MOE_OK;
-    SimtProduct p{};
-    p.P = x;
-    p.Q = w;
-    p.p_rs = l.ld_x;
-    p.q_rs = l.ld_w;
-    p.p_ks = p.q_ks = 1;
-    p.p_f32 = p.q_f32 = l.f32;
-    p.R = l.M;
-    p.C = l.N;
-    p.K = l.K;
-    p.epi = LinEpilogue{bias, residual, z, y, l.ld_y, l.ld_r, l.ld_z, l.act, l.of32, l.f32};
-    return launch_linear_simt(p, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const LinEpilogue epi{bias, residual, z, y, l.ld_y, l.ld_r, l.ld_z, l.act, l.of32, l.f32};
+    if (!l.f32) {
+        char* ws = static_cast<char*>(workspace);
+        const Rows xr = packed(x, l.M, l.K, l.ld_x, ws, st), wr = packed(w, l.N, l.K, l.ld_w, ws, st);
+        return launch_linear_tc(TcProduct{wr.p, xr.p, wr.ld, xr.ld, 0, 0, 1, 0, l.M, l.N, l.K, epi}, st);
+    }
+    return launch_linear_simt(SimtProduct{static_cast<const float*>(x), static_cast<const float*>(w), l.ld_x, 1, l.ld_w, 1, l.M, l.N, l.K, epi}, st);
 }
 
 moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const void* w, const void* z, const void* dy,
@@ -200,8 +247,12 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         if (dw && (s = zero_rows(dw, (size_t)l.N * l.K * (l.gf32 ? 4 : 2), st)) != MOE_OK) return s;
         return db ? zero_rows(db, (size_t)l.N * 4, st) : MOE_OK;
     }
-    float* dz = b.dz ? static_cast<float*>(workspace) : nullptr;
-    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + b.dz);
+    char* ws = static_cast<char*>(workspace);
+    void* dz = b.dz && (dx || dw) ? ws : nullptr;
+    float* part = reinterpret_cast<float*>(ws + b.dz);
+    ws += b.dz + b.part;
+    const int parts = dz_parts(l);
+    const long long ld_dz = l.f32 ? l.N : up8(l.N), plane = (long long)l.M * ld_dz;
     if (dz || db) {
         DzArgs a{};
         a.dy = dy;
@@ -209,12 +260,15 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         a.dz = dz;
         a.ld_dy = l.ld_y;
         a.ld_z = l.ld_z;
-        a.ld_dz = l.N;
+        a.ld_dz = ld_dz;
+        a.plane = plane;
         a.M = l.M;
         a.N = l.N;
         a.act = l.act;
         a.dy_f32 = l.of32;
         a.z_f32 = l.f32;
+        a.dz_f32 = l.f32;
+        a.parts = dw ? parts : 1;
         const int chunks = dz_chunks(l, &a.rows);
         a.part = db ? (chunks == 1 ? db : part) : nullptr;
         linear_dz_kernel<<<dim3(cdiv(l.N, DZ_COLS), chunks), DZ_THREADS, 0, st>>>(a);
@@ -225,40 +279,26 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         }
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     }
-    const void* g = dz ? static_cast<const void*>(dz) : dy;
-    const int g_f32 = dz ? 1 : l.of32;
-    const long long ld_g = dz ? l.N : l.ld_y;
+    const Rows g{b.dz ? dz : dy, b.dz ? ld_dz : l.ld_y};
     if (dx) {
-        SimtProduct p{};
-        p.P = g;
-        p.p_rs = ld_g;
-        p.p_ks = 1;
-        p.Q = w;
-        p.q_rs = 1;
-        p.q_ks = l.ld_w;
-        p.p_f32 = g_f32;
-        p.q_f32 = l.f32;
-        p.R = l.M;
-        p.C = l.K;
-        p.K = l.N;
-        p.epi = LinEpilogue{nullptr, nullptr, nullptr, dx, l.ld_dx, 0, 0, MOE_ACT_NONE, l.f32, 0};
-        if ((s = launch_linear_simt(p, st)) != MOE_OK) return s;
+        const LinEpilogue epi{nullptr, nullptr, nullptr, dx, l.ld_dx, 0, 0, MOE_ACT_NONE, l.f32, 0};
+        if (l.f32) {
+            s = launch_linear_simt(SimtProduct{static_cast<const float*>(g.p), static_cast<const float*>(w), g.ld, 1, 1, l.ld_w, l.M, l.K, l.N, epi}, st);
+        } else {
+            const Rows wr = packed(w, l.N, l.K, l.ld_w, ws, st);
+            s = launch_linear_tc(TcProduct{wr.p, g.p, wr.ld, g.ld, 1, 0, 1, 0, l.M, l.K, l.N, epi}, st);
+        }
+        if (s != MOE_OK) return s;
     }
     if (dw) {
-        SimtProduct p{};
-        p.P = g;
-        p.p_rs = 1;
-        p.p_ks = ld_g;
-        p.Q = x;
-        p.q_rs = 1;
-        p.q_ks = l.ld_x;
-        p.p_f32 = g_f32;
-        p.q_f32 = l.f32;
-        p.R = l.N;
-        p.C = l.K;
-        p.K = l.M;
-        p.epi = LinEpilogue{nullptr, nullptr, nullptr, dw, l.K, 0, 0, MOE_ACT_NONE, l.gf32, 0};
-        if ((s = launch_linear_simt(p, st)) != MOE_OK) return s;
+        const LinEpilogue epi{nullptr, nullptr, nullptr, dw, l.K, 0, 0, MOE_ACT_NONE, l.gf32, 0};
+        if (l.f32) {
+            s = launch_linear_simt(SimtProduct{static_cast<const float*>(g.p), static_cast<const float*>(x), 1, g.ld, 1, l.ld_x, l.N, l.K, l.M, epi}, st);
+        } else {
+            const Rows xr = packed(x, l.M, l.K, l.ld_x, ws, st);
+            s = launch_linear_tc(TcProduct{xr.p, g.p, xr.ld, g.ld, 1, 1, parts, plane, l.N, l.K, l.M, epi}, st);
+        }
+        if (s != MOE_OK) return s;
     }
     return MOE_OK;
 }

@@ -67,15 +67,31 @@ __device__ __forceinline__ void lin_store(const LinEpilogue& e, long long r, int
     else static_cast<__nv_bfloat16*>(e.out)[r * e.ld_out + c] = __float2bfloat16_rn(v);
 }
 
-// out[r, c] = epi(sum_k P(r, k) Q(c, k)), element (r, k) of P at r * p_rs + k * p_ks (one of them 1), Q alike.
+// fp32: out[r, c] = epi(sum_k P(r, k) Q(c, k)), element (r, k) of P at r * p_rs + k * p_ks (one of them 1), Q alike.
 struct SimtProduct {
-    const void* P;
-    const void* Q;
+    const float* P;
+    const float* Q;
     long long p_rs, p_ks, q_rs, q_ks;
-    int p_f32, q_f32;
     int R, C, K;
     LinEpilogue epi;
 };
 moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st);
+
+// The same product of bf16 operands on tensor cores.  A is the side that runs
+// along out's contiguous dimension (C), B the other (R).  An operand is either
+// K-major (its contraction index is contiguous: element (i, k) at i * ld + k) or
+// MN-major (at k * ld + i).  Bases 16-byte aligned, ld a multiple of 8.
+//   b_parts > 1: B is the sum of that many bf16 planes, b_plane elements apart.
+struct TcProduct {
+    const void* A;
+    const void* B;
+    long long lda, ldb;
+    int a_mn, b_mn;
+    int b_parts;
+    long long b_plane;
+    int R, C, K;
+    LinEpilogue epi;
+};
+moe_status launch_linear_tc(const TcProduct& p, cudaStream_t st);
 
 }  // namespace moe

@@ -16,17 +16,10 @@ namespace {
 constexpr int LS_THREADS = 256;
 constexpr int LS_BK = 16;
 
-template <typename T>
-__device__ __forceinline__ float as_f32(T v)
-{
-    if constexpr (sizeof(T) == 2) return __bfloat162float(v);
-    else return v;
-}
-
 // A TILE x 16 piece of an operand into registers: threads run along the
 // dimension that is contiguous in memory.
-template <typename T, int TILE>
-__device__ __forceinline__ void fetch(const T* base, long long rs, long long ks, int r0, int rows, int k0, int k1,
+template <int TILE>
+__device__ __forceinline__ void fetch(const float* base, long long rs, long long ks, int r0, int rows, int k0, int k1,
                                       float (&v)[TILE / 16])
 {
     const int t = threadIdx.x;
@@ -34,7 +27,7 @@ __device__ __forceinline__ void fetch(const T* base, long long rs, long long ks,
     for (int i = 0; i < TILE / 16; ++i) {
         const int r = ks == 1 ? t / LS_BK + (LS_THREADS / LS_BK) * i : t % TILE;
         const int k = ks == 1 ? t % LS_BK : t / TILE + (LS_THREADS / TILE) * i;
-        v[i] = (r0 + r < rows && k0 + k < k1) ? as_f32(base[(long long)(r0 + r) * rs + (long long)(k0 + k) * ks]) : 0.f;
+        v[i] = (r0 + r < rows && k0 + k < k1) ? base[(long long)(r0 + r) * rs + (long long)(k0 + k) * ks] : 0.f;
     }
 }
 
@@ -52,7 +45,7 @@ __device__ __forceinline__ void stash(float (*s)[TILE + 4], long long ks, const 
 
 // One TILE x TILE output tile per cluster; the cluster's blocks split K and add
 // their partial tiles in order of rank through distributed shared memory.
-template <typename TP, typename TQ, int TILE>
+template <int TILE>
 __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProduct p, int splits, int tiles_c)
 {
     constexpr int F = TILE / 16;                 // outputs per thread and direction
@@ -63,8 +56,6 @@ __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProdu
     const int r0 = (tile / tiles_c) * TILE, c0 = (tile % tiles_c) * TILE;
     const int blocks_k = cdiv(p.K, LS_BK);
     const int kb0 = (int)((long long)blocks_k * rank / splits), kb1 = (int)((long long)blocks_k * (rank + 1) / splits);
-    const TP* P = static_cast<const TP*>(p.P);
-    const TQ* Q = static_cast<const TQ*>(p.Q);
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     float acc[F][F];
 #pragma unroll
@@ -73,8 +64,8 @@ __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProdu
         for (int j = 0; j < F; ++j) acc[i][j] = 0.f;
     float vp[F], vq[F];
     if (kb0 < kb1) {
-        fetch<TP, TILE>(P, p.p_rs, p.p_ks, r0, p.R, kb0 * LS_BK, p.K, vp);
-        fetch<TQ, TILE>(Q, p.q_rs, p.q_ks, c0, p.C, kb0 * LS_BK, p.K, vq);
+        fetch<TILE>(p.P, p.p_rs, p.p_ks, r0, p.R, kb0 * LS_BK, p.K, vp);
+        fetch<TILE>(p.Q, p.q_rs, p.q_ks, c0, p.C, kb0 * LS_BK, p.K, vq);
     }
     int buf = 0;
     for (int kb = kb0; kb < kb1; ++kb, buf ^= 1) {
@@ -82,8 +73,8 @@ __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProdu
         stash<TILE>(sq[buf], p.q_ks, vq);
         __syncthreads();
         if (kb + 1 < kb1) {
-            fetch<TP, TILE>(P, p.p_rs, p.p_ks, r0, p.R, (kb + 1) * LS_BK, p.K, vp);
-            fetch<TQ, TILE>(Q, p.q_rs, p.q_ks, c0, p.C, (kb + 1) * LS_BK, p.K, vq);
+            fetch<TILE>(p.P, p.p_rs, p.p_ks, r0, p.R, (kb + 1) * LS_BK, p.K, vp);
+            fetch<TILE>(p.Q, p.q_rs, p.q_ks, c0, p.C, (kb + 1) * LS_BK, p.K, vq);
         }
 #pragma unroll
         for (int k = 0; k < LS_BK; ++k) {
@@ -130,14 +121,14 @@ __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProdu
     cl.sync();
 }
 
-template <typename TP, typename TQ, int TILE>
+template <int TILE>
 moe_status launch(const SimtProduct& p, int splits, cudaStream_t st)
 {
     const int tiles_c = cdiv(p.C, TILE);
     const long long tiles = (long long)cdiv(p.R, TILE) * tiles_c;
     if (tiles * splits >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
     const int smem = std::max(4 * LS_BK * (TILE + 4) * 4, splits > 1 ? TILE * TILE * 4 : 0);
-    auto* fn = linear_simt_kernel<TP, TQ, TILE>;
+    auto* fn = linear_simt_kernel<TILE>;
     if (ensure_smem_attr(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return MOE_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(tiles * splits));
@@ -154,25 +145,17 @@ moe_status launch(const SimtProduct& p, int splits, cudaStream_t st)
     return e == cudaSuccess ? cuda_status(cudaGetLastError()) : MOE_ERR_CUDA;
 }
 
-template <typename TP, typename TQ>
-moe_status pick(const SimtProduct& p, cudaStream_t st)
-{
-    const long long big = (long long)cdiv(p.R, 128) * cdiv(p.C, 128);
-    const int sms = num_sms();
-    if (big >= 2 * sms) return launch<TP, TQ, 128>(p, 1, st);
-    const long long tiles = (long long)cdiv(p.R, 64) * cdiv(p.C, 64);
-    int splits = 1;
-    while (splits < 8 && tiles * splits < sms && p.K >= 64 * splits) splits *= 2;
-    return launch<TP, TQ, 64>(p, splits, st);
-}
-
 }  // namespace
 
 moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st)
 {
-    if (p.p_f32 && p.q_f32) return pick<float, float>(p, st);
-    if (p.p_f32) return pick<float, __nv_bfloat16>(p, st);
-    return pick<__nv_bfloat16, __nv_bfloat16>(p, st);
+    const long long big = (long long)cdiv(p.R, 128) * cdiv(p.C, 128);
+    const int sms = num_sms();
+    if (big >= 2 * sms) return launch<128>(p, 1, st);
+    const long long tiles = (long long)cdiv(p.R, 64) * cdiv(p.C, 64);
+    int splits = 1;
+    while (splits < 8 && tiles * splits < sms && p.K >= 64 * splits) splits *= 2;
+    return launch<64>(p, splits, st);
 }
 
 }  // namespace moe

@@ -1,0 +1,651 @@
+// linear_tc.cu -- the dense product of bf16 operands on 5th-generation tensor
+// cores: out[r, c] = epi(sum_k B(r, k) A(c, k)), c contiguous in memory.
+//
+// The side that runs along out's contiguous dimension is the MMA's M side, so
+// a TMEM lane is one column c of the output and a TMEM column one row r: 32
+// lanes store 32 neighbouring elements of a row whatever the row stride is, a
+// bias is one value per lane, and no staging in shared memory is needed.  With
+// this orientation the three products of a layer differ only in which index of
+// an operand is contiguous:
+//   y  = x W^T    A = W   K-major    B = x    K-major
+//   dx = dz W     A = W^T MN-major   B = dz   K-major
+//   dw = dz^T x   A = x^T MN-major   B = dz^T MN-major
+// MN-major tiles are loaded as they lie in memory (64 contiguous elements x 64
+// steps of the contraction per box) and the MMA reads them through descriptors
+// of that order, so nothing is transposed.
+//
+// Two forms:
+//   pair    256 (c) x bn (r) tiles on CTA pairs (cta_group::2), persistent, two
+//           accumulators in TMEM, so a tile's epilogue runs under the next one's
+//           MMAs.
+//   split   128 (c) x bn (r) tiles of one CTA; a cluster of S CTAs splits the
+//           contraction and adds the partial tiles through distributed shared
+//           memory in order of rank (few rows, or few output tiles).
+
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "linear.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int KB = 64;                          // contraction elements per stage: 128-byte rows
+constexpr int CB = 128;                         // output columns of one CTA's tile (TMEM lanes)
+constexpr int A_BYTES = CB * KB * 2;            // 16 KB
+constexpr int BOX_BYTES = 64 * 128;             // an MN-major box: 64 steps of k x 64 elements
+
+struct TcArgs {
+    int R, C, nkb, bn;
+    int tiles_r, tiles_c, group_r;
+    int stages, splits, per_log;                // split form; log2 of the rows that each CTA of a cluster finishes
+    uint32_t b_bytes;                           // B bytes of one stage, part and CTA
+    LinEpilogue epi;
+};
+
+// Descriptor of an MN-major tile with 128-byte swizzle: 8 steps of the
+// contraction x 64 elements are 1024 B (stride offset), the next 64 elements
+// BOX_BYTES further (leading offset).  16 steps of the contraction: 2048 B.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(BOX_BYTES >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(const void* p)
+{
+    return MN ? sw128_mnmajor_desc(smem_u32(p)) : sw128_kmajor_desc(smem_u32(p));
+}
+template <bool MN>
+constexpr uint32_t kStepDesc = MN ? 2048u >> 4 : 32u >> 4;     // 16 elements of the contraction
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar_cluster, int c0, int c1,
+                                                 int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_t(float z)
+{
+    return act_apply(z, ACT);
+}
+
+// 32 accumulator columns of this lane: rows r0 .. r0 + 31 of column c.
+// nr: rows of them that exist; cv: the column exists.
+template <int ACT>
+__device__ __forceinline__ void epilogue32(const LinEpilogue& e, const uint32_t (&acc)[32], long long r0, int nr, int c,
+                                           bool cv, float bias)
+{
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) + bias;
+    if (e.z) {
+        __nv_bfloat16* z = static_cast<__nv_bfloat16*>(e.z) + r0 * e.ld_z + c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (cv && i < nr) z[i * e.ld_z] = __float2bfloat16_rn(v[i]);
+    }
+    if (e.residual) {
+        float res[32];
+        if (e.out_f32) {
+            const float* p = static_cast<const float*>(e.residual) + r0 * e.ld_r + c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) res[i] = cv && i < nr ? p[i * e.ld_r] : 0.f;
+        } else {
+            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.residual) + r0 * e.ld_r + c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) res[i] = cv && i < nr ? __bfloat162float(p[i * e.ld_r]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]) + res[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]);
+    }
+    if (e.out_f32) {
+        float* p = static_cast<float*>(e.out) + r0 * e.ld_out + c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (cv && i < nr) p[i * e.ld_out] = v[i];
+    } else {
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(e.out) + r0 * e.ld_out + c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (cv && i < nr) p[i * e.ld_out] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// ------------------------------------------------------------ pair form
+constexpr int PR_STAGES = 7;
+constexpr int PR_B_BYTES = 128 * KB * 2;                       // at most 128 rows of B per CTA
+constexpr int PR_STAGE = A_BYTES + PR_B_BYTES;
+constexpr int PR_EPI_WARPS = 8;                                // two per TMEM lane quarter, alternate 32-column chunks
+constexpr int PR_THREADS = 64 + 32 * PR_EPI_WARPS;
+constexpr int PR_SMEM = 1024 + PR_STAGES * PR_STAGE + 256;
+static_assert(PR_SMEM <= 232448, "shared memory per block");
+
+// Tile order: bands of group_r row tiles, inside a band the row tiles of one
+// column tile after another, so the pairs that run together share operands in L2.
+__device__ __forceinline__ void tile_at(const TcArgs& a, int tile, int& tr, int& tc)
+{
+    const int band = tile / (a.group_r * a.tiles_c);
+    const int in = tile - band * a.group_r * a.tiles_c;
+    const int h = min(a.group_r, a.tiles_r - band * a.group_r);
+    tc = in / h;
+    tr = band * a.group_r + in - tc * h;
+}
+
+template <bool AMN, bool BMN, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ TcArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + PR_STAGES * A_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + PR_STAGES * PR_STAGE);
+    uint64_t* empty = full + PR_STAGES;
+    uint64_t* acc_full = empty + PR_STAGES;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* mma_done = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+    const int total = a.tiles_r * a.tiles_c;
+
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < PR_STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 2 * PR_EPI_WARPS); }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) { tmem_alloc_pair(tmem_slot, 512); tmem_relinquish_pair(); }
+    if (threadIdx.x == 64) { tma_prefetch_desc(&tmA); tma_prefetch_desc(&tmB); }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+    const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
+    const int bh = a.bn / 2;                                   // rows of B in this CTA
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool bad = false;
+            for (int tile = cluster; tile < total && !bad; tile += n_clusters) {
+                int tr, tc;
+                tile_at(a, tile, tr, tc);
+                const int c0 = tc * 2 * CB + (int)rank * CB, r0 = tr * a.bn + (int)rank * bh;
+                if (*abort_flag) { bad = true; break; }
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!mbar_wait(&empty[s], ph ^ 1)) { *abort_flag = 1; bad = true; break; }
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * (A_BYTES + a.b_bytes));
+                    uint8_t* pa = sA + s * A_BYTES;
+                    uint8_t* pb = sB + s * PR_B_BYTES;
+                    const uint32_t bar = full_leader + 8 * s;
+                    if constexpr (AMN) {
+                        tma_load_2d_pair(pa, &tmA, bar, c0, kb * KB);
+                        tma_load_2d_pair(pa + BOX_BYTES, &tmA, bar, c0 + 64, kb * KB);
+                    } else {
+                        tma_load_2d_pair(pa, &tmA, bar, kb * KB, c0);
+                    }
+                    if constexpr (BMN) {
+                        tma_load_3d_pair(pb, &tmB, bar, r0, kb * KB, 0);
+                        if (bh > 64) tma_load_3d_pair(pb + BOX_BYTES, &tmB, bar, r0 + 64, kb * KB, 0);
+                    } else {
+                        tma_load_3d_pair(pb, &tmB, bar, kb * KB, r0, 0);
+                    }
+                    if (++s == PR_STAGES) { s = 0; ph ^= 1; }
+                }
+            }
+            if (bad) {   // copies already issued land within microseconds; let them
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 200000ull) { }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            const uint32_t idesc = idesc_bf16_f32(2 * CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+            const uint64_t ad0 = operand_desc<AMN>(sA), bd0 = operand_desc<BMN>(sB);
+            int s = 0, acc = 0;
+            uint32_t ph = 0, aph = 0;
+            bool bad = false;
+            for (int tile = cluster; tile < total && !bad; tile += n_clusters) {
+                if (*abort_flag || !mbar_wait(&acc_empty[acc], aph ^ 1)) { *abort_flag = 1; break; }
+                tc_fence_after();
+                const uint32_t d = tmem_base + acc * 256;
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!mbar_wait(&full[s], ph)) { *abort_flag = 1; bad = true; break; }
+                    const uint64_t ad = ad0 + (uint64_t)(s * (A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (PR_B_BYTES >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < KB / 16; ++kk)
+                        tc_mma_bf16_pair(d, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, (kb | kk) != 0);
+                    tc_commit_pair(&empty[s], 0x3);
+                    if (++s == PR_STAGES) { s = 0; ph ^= 1; }
+                }
+                if (bad) break;
+                tc_commit_pair(&acc_full[acc], 0x3);
+                if (++acc == 2) { acc = 0; aph ^= 1; }
+            }
+            // every MMA issued has completed before the CTAs may leave
+            tc_commit_pair(mma_done, 0x1);
+            mbar_wait(mma_done, 0);
+        }
+    } else {
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        int acc = 0;
+        uint32_t aph = 0;
+        for (int tile = cluster; tile < total; tile += n_clusters) {
+            int tr, tc;
+            tile_at(a, tile, tr, tc);
+            const int c = tc * 2 * CB + (int)rank * CB + q * 32 + lane;
+            const bool cv = c < a.C;
+            const long long r0 = (long long)tr * a.bn;
+            const int rows = (int)min((long long)a.bn, a.R - r0);
+            const float bias = a.epi.bias && cv ? a.epi.bias[c] : 0.f;
+            if (*abort_flag || !mbar_wait(&acc_full[acc], aph)) { *abort_flag = 1; break; }
+            tc_fence_after();
+            const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+            for (int j = half * 32; j < rows; j += 64) {
+                uint32_t v[32];
+                tmem_ld32(t + j, v);
+                tc_wait_ld_regs(v);
+                epilogue32<ACT>(a.epi, v, r0 + j, rows - j, c, cv, bias);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8 * acc);
+            if (++acc == 2) { acc = 0; aph ^= 1; }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();          // all MMAs done and all TMEM reads issued in both CTAs
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ------------------------------------------------------------ split form
+constexpr int SP_THREADS = 192;
+constexpr int SP_MAX_STAGES = 12;
+
+__host__ __device__ constexpr int sp_tmem_cols(int bn) { return bn <= 32 ? 32 : bn <= 64 ? 64 : bn <= 128 ? 128 : 256; }
+
+// Shared memory: stages x (A, then the parts of B), the partial sums that the
+// cluster's CTAs send here ([splits][bn / splits][128] fp32), the barriers.
+template <bool AMN, bool BMN, int ACT, int PARTS>
+__global__ void __launch_bounds__(SP_THREADS)
+linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ TcArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t stage_bytes = A_BYTES + PARTS * a.b_bytes;
+    float* red = reinterpret_cast<float*>(smem + (size_t)a.stages * stage_bytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + (a.splits > 1 ? a.bn * CB * 4 : 0));
+    uint64_t* empty = full + SP_MAX_STAGES;
+    uint64_t* acc_full = empty + SP_MAX_STAGES;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
+    const int tr = tile % a.tiles_r, tc = tile / a.tiles_r;
+    const int c0 = tc * CB;
+    const long long r0 = (long long)tr * a.bn;
+    const int kb0 = (int)((long long)a.nkb * rank / a.splits), kb1 = (int)((long long)a.nkb * (rank + 1) / a.splits);
+    const int cols = sp_tmem_cols(a.bn);
+
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) { tmem_alloc(tmem_slot, cols); tmem_relinquish(); }
+    if (threadIdx.x == 64) { tma_prefetch_desc(&tmA); tma_prefetch_desc(&tmB); }
+    tc_fence_before();
+    __syncthreads();
+    if (a.splits > 1) cluster_sync_all();          // the peers' shared memory exists before anything is sent there
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool bad = false;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&empty[s], ph ^ 1)) { *abort_flag = 1; bad = true; break; }
+                mbar_arrive_expect_tx(&full[s], stage_bytes);
+                uint8_t* pa = smem + (size_t)s * stage_bytes;
+                uint8_t* pb = pa + A_BYTES;
+                if constexpr (AMN) {
+                    tma_load_2d(pa, &tmA, &full[s], c0, kb * KB);
+                    tma_load_2d(pa + BOX_BYTES, &tmA, &full[s], c0 + 64, kb * KB);
+                } else {
+                    tma_load_2d(pa, &tmA, &full[s], kb * KB, c0);
+                }
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p, pb += a.b_bytes) {
+                    if constexpr (BMN) {
+                        for (int h = 0; h < a.bn; h += 64)
+                            tma_load_3d(pb + h * (BOX_BYTES / 64), &tmB, &full[s], (int)r0 + h, kb * KB, p);
+                    } else {
+                        tma_load_3d(pb, &tmB, &full[s], kb * KB, (int)r0, p);
+                    }
+                }
+                if (++s == a.stages) { s = 0; ph ^= 1; }
+            }
+            if (bad) {
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 200000ull) { }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16_f32(CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&full[s], ph)) { *abort_flag = 1; break; }
+                const uint8_t* pa = smem + (size_t)s * stage_bytes;
+                const uint64_t ad = operand_desc<AMN>(pa);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) {
+                    const uint64_t bd = operand_desc<BMN>(pa + A_BYTES + p * a.b_bytes);
+#pragma unroll
+                    for (int kk = 0; kk < KB / 16; ++kk)
+                        tc_mma_bf16(tmem_base, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc,
+                                    kb > kb0 || p > 0 || kk > 0);
+                }
+                tc_commit(&empty[s]);
+                if (++s == a.stages) { s = 0; ph ^= 1; }
+            }
+            tc_commit(acc_full);
+        }
+    } else {
+        const int q = warp & 3;
+        const int c = c0 + q * 32 + lane;
+        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16);
+        const bool ok = mbar_wait(acc_full, 0) && !*abort_flag;
+        tc_fence_after();
+        if (!ok) {
+            *abort_flag = 1;
+        } else if (a.splits == 1) {
+            const bool cv = c < a.C;
+            const int rows = (int)min((long long)a.bn, a.R - r0);
+            const float bias = a.epi.bias && cv ? a.epi.bias[c] : 0.f;
+            for (int j = 0; j < rows; j += 32) {
+                uint32_t v[32];
+                tmem_ld32(t + j, v);               // (bn = 16: the upper half is not used, the allocation has 32 columns)
+                tc_wait_ld_regs(v);
+                epilogue32<ACT>(a.epi, v, r0 + j, rows - j, c, cv, bias);
+            }
+        } else {
+            // row j of the tile is finished by CTA j >> per_log; it gets this CTA's partial sums of it
+            const uint32_t mine = smem_u32(red) + (uint32_t)((((rank << a.per_log) * CB) + q * 32 + lane) * 4);
+            for (int j0 = 0; j0 < a.bn; j0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(t + j0, v);
+                tc_wait_ld_regs(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int j = j0 + i;
+                    if (j < a.bn)
+                        st_cluster_f32(mapa_shared(mine + (uint32_t)((j & ((1 << a.per_log) - 1)) * CB * 4), j >> a.per_log),
+                                       __uint_as_float(v[i]));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, cols);
+    }
+    if (a.splits == 1) return;
+    cluster_sync_all();                            // every partial sum has arrived
+    const int per = 1 << a.per_log;
+    const long long rb = r0 + (long long)rank * per;
+    // a warp finishes 32 columns of a row at a time
+    for (int u = warp; u < per * (CB / 32); u += SP_THREADS / 32) {
+        const int j = u / (CB / 32), cc = (u % (CB / 32)) * 32 + lane, c = c0 + cc;
+        float v = 0.f;
+        for (int s = 0; s < a.splits; ++s) v += red[(s * per + j) * CB + cc];
+        if (rb + j < a.R && c < a.C) {
+            LinEpilogue e = a.epi;
+            e.act = ACT;
+            lin_store(e, rb + j, c, v);
+        }
+    }
+}
+
+// ------------------------------------------------------------ host
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// An operand as [planes][outer][inner] with 128-byte swizzled boxes of 64 x box_outer.
+bool operand_map(CUtensorMap* m, const void* base, int inner, int outer, long long ld, int planes, long long plane,
+                 int box_outer)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(planes > 1 ? plane : ld * outer) * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_outer, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+    int pair, bn, splits, stages, occ;
+};
+
+int sp_stage_bytes(const TcProduct& p, int bn)
+{
+    const int b = p.b_mn ? cdiv(bn, 64) * BOX_BYTES : bn * 128;
+    return A_BYTES + p.b_parts * b;
+}
+
+// Shared memory of a split-form block with `occ` blocks per SM; 0 stages if it does not fit.
+int sp_stages(const TcProduct& p, int bn, int splits, int occ)
+{
+    const int room = (occ == 2 ? 113 : 226) * 1024 - 1024 - 512 - (splits > 1 ? bn * CB * 4 : 0);
+    return std::min(SP_MAX_STAGES, room / sp_stage_bytes(p, bn));
+}
+
+// Which form and tile: the smallest estimate of the SM clocks.  Per 64-wide step
+// of the contraction a CTA's MMAs take 2 bn clocks (pair: 256 x bn on two SMs,
+// split: 128 x bn on one at half of that), its loads its bytes over ~64 B per
+// clock and SM from L2.
+Plan choose(const TcProduct& p)
+{
+    const int nkb = cdiv(p.K, KB), sms = num_sms();
+    Plan best{};
+    double least = 1e30;
+    if (p.b_parts == 1) {
+        const int tc = cdiv(p.C, 2 * CB);
+        for (int bn = 64; bn <= 256; bn += 32) {
+            const long long tiles = (long long)tc * cdiv(p.R, bn);
+            const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
+            const double step = std::max(2.0 * bn, (A_BYTES + bn * 64) / 64.0);
+            const double t = waves * (nkb * step + 300) + 5000 + 10 * bn;
+            if (t < least) { least = t; best = Plan{1, bn, 1, PR_STAGES, 1}; }
+        }
+    }
+    const int tc = cdiv(p.C, CB);
+    for (int bn : {16, 32, 64, 128}) {
+        if (p.b_parts > 1 && bn > 64) continue;
+        const long long tiles = (long long)tc * cdiv(p.R, bn);
+        for (int S = 1; S <= 8; S *= 2) {
+            if (S > nkb || bn / S < 1) continue;
+            const int occ = sp_stages(p, bn, S, 2) >= 3 ? 2 : 1;
+            const int stages = sp_stages(p, bn, S, occ);
+            if (stages < 2) continue;
+            const long long waves = (tiles * S + (long long)sms * occ - 1) / ((long long)sms * occ);
+            const double step = occ * std::max(2.0 * bn * p.b_parts, sp_stage_bytes(p, bn) / 64.0);
+            const double t = waves * (cdiv(nkb, S) * step + 3000 + 16 * bn + (S > 1 ? 2500 + 8 * bn : 0)) + 2000;
+            if (t < least) { least = t; best = Plan{0, bn, S, stages, occ}; }
+        }
+    }
+    return best;
+}
+
+template <bool AMN, bool BMN, int ACT>
+moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
+{
+    CUtensorMap mA, mB;
+    TcArgs a{};
+    a.R = p.R;
+    a.C = p.C;
+    a.nkb = cdiv(p.K, KB);
+    a.bn = pl.bn;
+    a.tiles_r = cdiv(p.R, pl.bn);
+    a.tiles_c = cdiv(p.C, 2 * CB);
+    a.group_r = 8;
+    a.epi = p.epi;
+    a.b_bytes = BMN ? cdiv(pl.bn / 2, 64) * BOX_BYTES : pl.bn / 2 * 128;
+    const long long tiles = (long long)a.tiles_r * a.tiles_c;
+    if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED;
+    if (!(AMN ? operand_map(&mA, p.A, p.C, p.K, p.lda, 0, 0, 64) : operand_map(&mA, p.A, p.K, p.C, p.lda, 0, 0, CB)))
+        return MOE_ERR_CUDA;
+    if (!(BMN ? operand_map(&mB, p.B, p.R, p.K, p.ldb, 1, 0, 64) : operand_map(&mB, p.B, p.K, p.R, p.ldb, 1, 0, pl.bn / 2)))
+        return MOE_ERR_CUDA;
+    auto* fn = linear_pair_kernel<AMN, BMN, ACT>;
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), PR_SMEM);
+    if (e != cudaSuccess) return cuda_status(e);
+    const int clusters = (int)std::min<long long>(tiles, num_sms() / 2);
+    fn<<<2 * clusters, PR_THREADS, PR_SMEM, st>>>(mA, mB, a);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+template <bool AMN, bool BMN, int ACT, int PARTS>
+moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
+{
+    CUtensorMap mA, mB;
+    TcArgs a{};
+    a.R = p.R;
+    a.C = p.C;
+    a.nkb = cdiv(p.K, KB);
+    a.bn = pl.bn;
+    a.tiles_r = cdiv(p.R, pl.bn);
+    a.tiles_c = cdiv(p.C, CB);
+    a.stages = pl.stages;
+    a.splits = pl.splits;
+    while ((pl.bn >> a.per_log) > pl.splits) ++a.per_log;
+    a.epi = p.epi;
+    a.b_bytes = BMN ? cdiv(pl.bn, 64) * BOX_BYTES : pl.bn * 128;
+    const long long ctas = (long long)a.tiles_r * a.tiles_c * pl.splits;
+    if (ctas >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+    if (!(AMN ? operand_map(&mA, p.A, p.C, p.K, p.lda, 0, 0, 64) : operand_map(&mA, p.A, p.K, p.C, p.lda, 0, 0, CB)))
+        return MOE_ERR_CUDA;
+    if (!(BMN ? operand_map(&mB, p.B, p.R, p.K, p.ldb, PARTS, p.b_plane, 64)
+              : operand_map(&mB, p.B, p.K, p.R, p.ldb, PARTS, p.b_plane, pl.bn)))
+        return MOE_ERR_CUDA;
+    auto* fn = linear_split_kernel<AMN, BMN, ACT, PARTS>;
+    const int smem = 1024 + pl.stages * sp_stage_bytes(p, pl.bn) + (pl.splits > 1 ? pl.bn * CB * 4 : 0) + 256;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem);
+    if (e != cudaSuccess) return cuda_status(e);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(SP_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)pl.splits, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fn, mA, mB, a);
+    count_launch();
+    return e == cudaSuccess ? cuda_status(cudaGetLastError()) : MOE_ERR_CUDA;
+}
+
+moe_status launch_plan(const TcProduct& p, const Plan& pl, cudaStream_t st)
+{
+    if (!p.a_mn && !p.b_mn && p.b_parts == 1) {
+        switch (p.epi.act) {
+            case MOE_ACT_NONE:
+                return pl.pair ? launch_pair<false, false, MOE_ACT_NONE>(p, pl, st) : launch_split<false, false, MOE_ACT_NONE, 1>(p, pl, st);
+            case MOE_ACT_RELU:
+                return pl.pair ? launch_pair<false, false, MOE_ACT_RELU>(p, pl, st) : launch_split<false, false, MOE_ACT_RELU, 1>(p, pl, st);
+            case MOE_ACT_SILU:
+                return pl.pair ? launch_pair<false, false, MOE_ACT_SILU>(p, pl, st) : launch_split<false, false, MOE_ACT_SILU, 1>(p, pl, st);
+            default:
+                return pl.pair ? launch_pair<false, false, MOE_ACT_GELU>(p, pl, st) : launch_split<false, false, MOE_ACT_GELU, 1>(p, pl, st);
+        }
+    }
+    if (p.epi.act != MOE_ACT_NONE) return MOE_ERR_UNSUPPORTED;
+    if (p.a_mn && !p.b_mn && p.b_parts == 1)
+        return pl.pair ? launch_pair<true, false, MOE_ACT_NONE>(p, pl, st) : launch_split<true, false, MOE_ACT_NONE, 1>(p, pl, st);
+    if (p.a_mn && p.b_mn && p.b_parts == 1)
+        return pl.pair ? launch_pair<true, true, MOE_ACT_NONE>(p, pl, st) : launch_split<true, true, MOE_ACT_NONE, 1>(p, pl, st);
+    if (p.a_mn && p.b_mn && p.b_parts == 3 && !pl.pair) return launch_split<true, true, MOE_ACT_NONE, 3>(p, pl, st);
+    return MOE_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+moe_status launch_linear_tc(const TcProduct& p, cudaStream_t st) { return launch_plan(p, choose(p), st); }
+
+}  // namespace moe
