@@ -86,6 +86,22 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
+// The producer and the MMA issuer are whole warps in uniform control flow, one
+// elected lane of which issues: the tensor-core and TMA instructions take their
+// operands from uniform registers, and code that a single lane had branched
+// into moved each operand there anew (~60 clocks per MMA).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -180,7 +196,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
@@ -205,17 +221,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     const int bh = a.bn / 2;                                   // rows of B in this CTA
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            bool bad = false;
-            for (int tile = cluster; tile < total && !bad; tile += n_clusters) {
-                int tr, tc;
-                tile_at(a, tile, tr, tc);
-                const int c0 = tc * 2 * CB + (int)rank * CB, r0 = tr * a.bn + (int)rank * bh;
-                if (*abort_flag) { bad = true; break; }
-                for (int kb = 0; kb < a.nkb; ++kb) {
-                    if (!mbar_wait(&empty[s], ph ^ 1)) { *abort_flag = 1; bad = true; break; }
+        int s = 0;
+        uint32_t ph = 0;
+        bool bad = false;
+        for (int tile = cluster; tile < total && !bad; tile += n_clusters) {
+            int tr, tc;
+            tile_at(a, tile, tr, tc);
+            const int c0 = tc * 2 * CB + (int)rank * CB, r0 = tr * a.bn + (int)rank * bh;
+            for (int kb = 0; kb < a.nkb; ++kb) {
+                if (!warp_wait(&empty[s], ph ^ 1)) { *abort_flag = 1; bad = true; break; }
+                if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(&full[s], 2 * (A_BYTES + a.b_bytes));
                     uint8_t* pa = sA + s * A_BYTES;
                     uint8_t* pb = sB + s * PR_B_BYTES;
@@ -232,40 +247,44 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     } else {
                         tma_load_3d_pair(pb, &tmB, bar, kb * KB, r0, 0);
                     }
-                    if (++s == PR_STAGES) { s = 0; ph ^= 1; }
                 }
-            }
-            if (bad) {   // copies already issued land within microseconds; let them
-                const uint64_t t0 = globaltimer();
-                while (globaltimer() - t0 < 200000ull) { }
+                __syncwarp();
+                if (++s == PR_STAGES) { s = 0; ph ^= 1; }
             }
         }
+        if (bad) {   // copies already issued land within microseconds; let them
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 200000ull) { }
+        }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             const uint32_t idesc = idesc_bf16_f32(2 * CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
             const uint64_t ad0 = operand_desc<AMN>(sA), bd0 = operand_desc<BMN>(sB);
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool bad = false;
             for (int tile = cluster; tile < total && !bad; tile += n_clusters) {
-                if (*abort_flag || !mbar_wait(&acc_empty[acc], aph ^ 1)) { *abort_flag = 1; break; }
+                if (!warp_wait(&acc_empty[acc], aph ^ 1)) { *abort_flag = 1; break; }
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * 256;
                 for (int kb = 0; kb < a.nkb; ++kb) {
-                    if (!mbar_wait(&full[s], ph)) { *abort_flag = 1; bad = true; break; }
+                    if (!warp_wait(&full[s], ph)) { *abort_flag = 1; bad = true; break; }
                     const uint64_t ad = ad0 + (uint64_t)(s * (A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (PR_B_BYTES >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < KB / 16; ++kk)
-                        tc_mma_bf16_pair(d, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, (kb | kk) != 0);
-                    tc_commit_pair(&empty[s], 0x3);
+                        for (int kk = 0; kk < KB / 16; ++kk)
+                            tc_mma_bf16_pair(d, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, (kb | kk) != 0);
+                        tc_commit_pair(&empty[s], 0x3);
+                        if (kb + 1 == a.nkb) tc_commit_pair(&acc_full[acc], 0x3);
+                    }
+                    __syncwarp();
                     if (++s == PR_STAGES) { s = 0; ph ^= 1; }
                 }
-                if (bad) break;
-                tc_commit_pair(&acc_full[acc], 0x3);
                 if (++acc == 2) { acc = 0; aph ^= 1; }
             }
             // every MMA issued has completed before the CTAs may leave
-            tc_commit_pair(mma_done, 0x1);
+            if (elect_one()) tc_commit_pair(mma_done, 0x1);
+            __syncwarp();
             mbar_wait(mma_done, 0);
         }
     } else {
@@ -328,7 +347,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
     const int tr = tile % a.tiles_r, tc = tile / a.tiles_r;
     const int c0 = tc * CB;
@@ -351,12 +370,12 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     const uint32_t tmem_base = *tmem_slot;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            bool bad = false;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&empty[s], ph ^ 1)) { *abort_flag = 1; bad = true; break; }
+        int s = 0;
+        uint32_t ph = 0;
+        bool bad = false;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(&empty[s], ph ^ 1)) { *abort_flag = 1; bad = true; break; }
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], stage_bytes);
                 uint8_t* pa = smem + (size_t)s * stage_bytes;
                 uint8_t* pb = pa + A_BYTES;
@@ -375,35 +394,37 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                         tma_load_3d(pb, &tmB, &full[s], kb * KB, (int)r0, p);
                     }
                 }
-                if (++s == a.stages) { s = 0; ph ^= 1; }
             }
-            if (bad) {
-                const uint64_t t0 = globaltimer();
-                while (globaltimer() - t0 < 200000ull) { }
-            }
+            __syncwarp();
+            if (++s == a.stages) { s = 0; ph ^= 1; }
+        }
+        if (bad) {
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 200000ull) { }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32(CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
-            int s = 0;
-            uint32_t ph = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&full[s], ph)) { *abort_flag = 1; break; }
-                const uint8_t* pa = smem + (size_t)s * stage_bytes;
-                const uint64_t ad = operand_desc<AMN>(pa);
+        const uint32_t idesc = idesc_bf16_f32(CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+        const uint64_t ad0 = operand_desc<AMN>(smem), bd0 = operand_desc<BMN>(smem + A_BYTES);
+        const uint32_t stage16 = stage_bytes >> 4, part16 = a.b_bytes >> 4;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(&full[s], ph)) { *abort_flag = 1; break; }
+            const uint64_t ad = ad0 + (uint64_t)(s * stage16), bd = bd0 + (uint64_t)(s * stage16);
+            if (elect_one()) {
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    const uint64_t bd = operand_desc<BMN>(pa + A_BYTES + p * a.b_bytes);
+                for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                     for (int kk = 0; kk < KB / 16; ++kk)
-                        tc_mma_bf16(tmem_base, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc,
+                        tc_mma_bf16(tmem_base, ad + kk * kStepDesc<AMN>, bd + p * part16 + kk * kStepDesc<BMN>, idesc,
                                     kb > kb0 || p > 0 || kk > 0);
-                }
                 tc_commit(&empty[s]);
-                if (++s == a.stages) { s = 0; ph ^= 1; }
             }
-            tc_commit(acc_full);
+            __syncwarp();
+            if (++s == a.stages) { s = 0; ph ^= 1; }
         }
+        if (elect_one()) tc_commit(acc_full);
+        __syncwarp();
     } else {
         const int q = warp & 3;
         const int c = c0 + q * 32 + lane;
@@ -497,7 +518,7 @@ bool operand_map(CUtensorMap* m, const void* base, int inner, int outer, long lo
 }
 
 struct Plan {
-    int pair, bn, splits, stages, occ;
+    int pair, bn, splits, stages, occ, group;
 };
 
 int sp_stage_bytes(const TcProduct& p, int bn)
@@ -529,7 +550,7 @@ Plan choose(const TcProduct& p)
             const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
             const double step = std::max(2.0 * bn, (A_BYTES + bn * 64) / 64.0);
             const double t = waves * (nkb * step + 300) + 5000 + 10 * bn;
-            if (t < least) { least = t; best = Plan{1, bn, 1, PR_STAGES, 1}; }
+            if (t < least) { least = t; best = Plan{1, bn, 1, PR_STAGES, 1, 8}; }
         }
     }
     const int tc = cdiv(p.C, CB);
@@ -544,7 +565,7 @@ Plan choose(const TcProduct& p)
             const long long waves = (tiles * S + (long long)sms * occ - 1) / ((long long)sms * occ);
             const double step = occ * std::max(2.0 * bn * p.b_parts, sp_stage_bytes(p, bn) / 64.0);
             const double t = waves * (cdiv(nkb, S) * step + 3000 + 16 * bn + (S > 1 ? 2500 + 8 * bn : 0)) + 2000;
-            if (t < least) { least = t; best = Plan{0, bn, S, stages, occ}; }
+            if (t < least) { least = t; best = Plan{0, bn, S, stages, occ, 1}; }
         }
     }
     return best;
@@ -561,7 +582,7 @@ moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
     a.bn = pl.bn;
     a.tiles_r = cdiv(p.R, pl.bn);
     a.tiles_c = cdiv(p.C, 2 * CB);
-    a.group_r = 8;
+    a.group_r = pl.group;
     a.epi = p.epi;
     a.b_bytes = BMN ? cdiv(pl.bn / 2, 64) * BOX_BYTES : pl.bn / 2 * 128;
     const long long tiles = (long long)a.tiles_r * a.tiles_c;

@@ -23,6 +23,9 @@ def make_linear_desc(M: int, N: int, K: int, dtype="bf16", act: str = "none", ou
                              ld_dx=ld_dx)
 
 
+_HERE = contextlib.nullcontext()
+
+
 class Linear:
     """A dense product with device-resident weights w [N, K] and bias [N] (fp32, or None).
 
@@ -46,10 +49,11 @@ class Linear:
     def _check(self, name, t, rows, cols, dtype) -> None:
         if t is None:
             return
-        if t.dim() != 2 or tuple(t.shape) != (rows, cols) or t.dtype != dtype:
+        if t.shape != (rows, cols) or t.dtype != dtype:
             raise ValueError(f"{name}: expected a [{rows}, {cols}] {dtype} tensor, got {list(t.shape)} {t.dtype}")
-        if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
-            raise ValueError(f"{name}: expected contiguous rows that do not overlap, got strides {tuple(t.stride())}")
+        s0, s1 = t.stride()
+        if cols > 1 and s1 != 1 or rows > 1 and s0 < cols:
+            raise ValueError(f"{name}: expected contiguous rows that do not overlap, got strides {(s0, s1)}")
         if t.device != self.w.device:
             raise ValueError(f"{name}: on {t.device}, the weights are on {self.w.device}")
 
@@ -68,8 +72,8 @@ class Linear:
         if not self.w.is_cuda:
             raise ValueError("libmoe takes CUDA tensors")
         if stream is None:
-            if self.w.device.index == torch.cuda.current_device():
-                return contextlib.nullcontext(), None
+            if self.w.get_device() == torch.cuda.current_device():
+                return _HERE, None
             return torch.cuda.device(self.w.device), None
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=self.w.device)
