@@ -43,8 +43,10 @@ struct TcArgs {
     int tiles_r, tiles_c, group_r;
     int stages, splits, per_log;                // split form; log2 of the rows that each CTA of a cluster finishes
     uint32_t b_bytes;                           // B bytes of one stage, part and CTA
+    int staged;                                 // ST_* bits: which bf16 tensors go through shared memory
     LinEpilogue epi;
 };
+constexpr int ST_OUT = 1, ST_Z = 2, ST_RES = 4;
 
 // Descriptor of an MN-major tile with 128-byte swizzle: 8 steps of the
 // contraction x 64 elements are 1024 B (stride offset), the next 64 elements
@@ -107,28 +109,100 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// Whether `ok` holds for all 128 threads of a named barrier's group.
+__device__ __forceinline__ bool group_and(bool ok, int bar)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)ok), "r"(bar) : "memory");
+    return r != 0;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_t(float z)
 {
     return act_apply(z, ACT);
 }
 
-// 32 accumulator columns of this lane: rows r0 .. r0 + 31 of column c.
+// 32 accumulator columns of this lane: rows r0 .. r0 + 31 of column c0 + cl.
 // nr: rows of them that exist; cv: the column exists.
+//
+// bf16 rows pass through shared memory: a lane's element is 2 bytes, so storing
+// it directly makes 64-byte pieces per warp (8.5 us per 256 x 256 tile, more than
+// a K = 512 tile's MMAs).  The four warps of a group (one per TMEM lane quarter)
+// lay a chunk of 32 rows x 128 columns into one of two 8 KB buffers, from which
+// one TMA store writes whole 256-byte rows and clips what lies outside the
+// tensor; a residual comes in through the same buffer by 16-byte loads.  Rows
+// that TMA cannot address (a stride that is not a multiple of 16 bytes) are
+// stored directly, and fp32 rows too (128 bytes per warp as it is).
+constexpr int STAGE_ROWS = 32 * CB * 2;
+struct Staging {
+    uint8_t* buf;            // two buffers of STAGE_ROWS bytes
+    int at;                  // the next one
+    int bar;                 // named barrier of the group's 128 threads
+    int tid;                 // thread of the group
+
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
+    // the next buffer, once the store that last used it has read it
+    __device__ __forceinline__ uint8_t* acquire()
+    {
+        if (tid == 0) bulk_wait_read<1>();
+        sync();
+        uint8_t* b = buf + at * STAGE_ROWS;
+        at ^= 1;
+        return b;
+    }
+    __device__ __forceinline__ void store(const CUtensorMap* m, const uint8_t* b, int c0, int r0) const
+    {
+        fence_proxy_async_smem();
+        sync();
+        if (tid == 0) {
+            tma_store_2d(m, b, c0, r0);
+            bulk_commit();
+        }
+    }
+};
+
 template <int ACT>
-__device__ __forceinline__ void epilogue32(const LinEpilogue& e, const uint32_t (&acc)[32], long long r0, int nr, int c,
-                                           bool cv, float bias)
+__device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* tmOut, const CUtensorMap* tmZ,
+                                           const uint32_t (&acc)[32], long long r0, int nr, int c0, int cl, float bias,
+                                           Staging& st)
 {
+    const LinEpilogue& e = a.epi;
+    const int c = c0 + cl;
+    const bool cv = c < a.C;
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) + bias;
-    if (e.z) {
+    if (a.staged & ST_Z) {
+        uint8_t* b = st.acquire();
+        __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + cl;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mine[i * CB] = __float2bfloat16_rn(v[i]);
+        st.store(tmZ, b, c0, (int)r0);
+    } else if (e.z) {
         __nv_bfloat16* z = static_cast<__nv_bfloat16*>(e.z) + r0 * e.ld_z + c;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             if (cv && i < nr) z[i * e.ld_z] = __float2bfloat16_rn(v[i]);
     }
-    if (e.residual) {
+    uint8_t* b = a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
+    __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + cl;
+    if (a.staged & ST_RES) {
+        const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(e.residual) + r0 * e.ld_r + c0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = k * 8 + st.tid / 16, u = st.tid % 16;
+            if (r < nr && c0 + u * 8 < a.C)
+                *reinterpret_cast<uint4*>(b + r * (CB * 2) + u * 16) =
+                    *reinterpret_cast<const uint4*>(res + r * e.ld_r + u * 8);
+        }
+        st.sync();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]) + __bfloat162float(mine[i * CB]);
+    } else if (e.residual) {
         float res[32];
         if (e.out_f32) {
             const float* p = static_cast<const float*>(e.residual) + r0 * e.ld_r + c;
@@ -145,7 +219,11 @@ __device__ __forceinline__ void epilogue32(const LinEpilogue& e, const uint32_t 
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]);
     }
-    if (e.out_f32) {
+    if (a.staged & ST_OUT) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mine[i * CB] = __float2bfloat16_rn(v[i]);
+        st.store(tmOut, b, c0, (int)r0);
+    } else if (e.out_f32) {
         float* p = static_cast<float*>(e.out) + r0 * e.ld_out + c;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -159,13 +237,17 @@ __device__ __forceinline__ void epilogue32(const LinEpilogue& e, const uint32_t 
 }
 
 // ------------------------------------------------------------ pair form
-constexpr int PR_STAGES = 7;
-constexpr int PR_B_BYTES = 128 * KB * 2;                       // at most 128 rows of B per CTA
-constexpr int PR_STAGE = A_BYTES + PR_B_BYTES;
-constexpr int PR_EPI_WARPS = 8;                                // two per TMEM lane quarter, alternate 32-column chunks
+constexpr int PR_MAX_STAGES = 10;
+constexpr int PR_EPI_WARPS = 8;                                // two per TMEM lane quarter, alternate 32-row chunks
 constexpr int PR_THREADS = 64 + 32 * PR_EPI_WARPS;
-constexpr int PR_SMEM = 1024 + PR_STAGES * PR_STAGE + 256;
-static_assert(PR_SMEM <= 232448, "shared memory per block");
+constexpr int PR_STAGING = 2 * 2 * STAGE_ROWS;                 // two groups of four warps
+constexpr int PR_SMEM = 227 * 1024;
+// as many stages as fit: 6 of 32 KB (bn = 256) to 9 of 20 KB (bn = 64)
+__host__ __device__ constexpr int pr_stages(int b_bytes)
+{
+    const int n = (PR_SMEM - 1024 - PR_STAGING - 512) / (A_BYTES + b_bytes);
+    return n < PR_MAX_STAGES ? n : PR_MAX_STAGES;
+}
 
 // Tile order: bands of group_r row tiles, inside a band the row tiles of one
 // column tile after another, so the pairs that run together share operands in L2.
@@ -181,16 +263,18 @@ __device__ __forceinline__ void tile_at(const TcArgs& a, int tile, int& tr, int&
 template <bool AMN, bool BMN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
                    const __grid_constant__ TcArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* sA = smem;
-    uint8_t* sB = smem + PR_STAGES * A_BYTES;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + PR_STAGES * PR_STAGE);
-    uint64_t* empty = full + PR_STAGES;
-    uint64_t* acc_full = empty + PR_STAGES;
+    uint8_t* staging = smem;
+    uint8_t* sA = smem + PR_STAGING;
+    uint8_t* sB = sA + a.stages * A_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + a.stages * a.b_bytes);
+    uint64_t* empty = full + PR_MAX_STAGES;
+    uint64_t* acc_full = empty + PR_MAX_STAGES;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* mma_done = acc_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -203,7 +287,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     const int total = a.tiles_r * a.tiles_c;
 
     if (threadIdx.x == 32) {
-        for (int s = 0; s < PR_STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 2 * PR_EPI_WARPS); }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -233,7 +317,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(&full[s], 2 * (A_BYTES + a.b_bytes));
                     uint8_t* pa = sA + s * A_BYTES;
-                    uint8_t* pb = sB + s * PR_B_BYTES;
+                    uint8_t* pb = sB + s * a.b_bytes;
                     const uint32_t bar = full_leader + 8 * s;
                     if constexpr (AMN) {
                         tma_load_2d_pair(pa, &tmA, bar, c0, kb * KB);
@@ -249,7 +333,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     }
                 }
                 __syncwarp();
-                if (++s == PR_STAGES) { s = 0; ph ^= 1; }
+                if (++s == a.stages) { s = 0; ph ^= 1; }
             }
         }
         if (bad) {   // copies already issued land within microseconds; let them
@@ -260,6 +344,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         if (leader) {
             const uint32_t idesc = idesc_bf16_f32(2 * CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
             const uint64_t ad0 = operand_desc<AMN>(sA), bd0 = operand_desc<BMN>(sB);
+            const uint32_t b16 = a.b_bytes >> 4;
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
             bool bad = false;
@@ -269,7 +354,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 const uint32_t d = tmem_base + acc * 256;
                 for (int kb = 0; kb < a.nkb; ++kb) {
                     if (!warp_wait(&full[s], ph)) { *abort_flag = 1; bad = true; break; }
-                    const uint64_t ad = ad0 + (uint64_t)(s * (A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (PR_B_BYTES >> 4));
+                    const uint64_t ad = ad0 + (uint64_t)(s * (A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * b16);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < KB / 16; ++kk)
@@ -278,7 +363,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                         if (kb + 1 == a.nkb) tc_commit_pair(&acc_full[acc], 0x3);
                     }
                     __syncwarp();
-                    if (++s == PR_STAGES) { s = 0; ph ^= 1; }
+                    if (++s == a.stages) { s = 0; ph ^= 1; }
                 }
                 if (++acc == 2) { acc = 0; aph ^= 1; }
             }
@@ -289,30 +374,33 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         }
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
+        const int cl = q * 32 + lane;
+        Staging st{staging + half * 2 * STAGE_ROWS, 0, 1 + half, cl};
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = cluster; tile < total; tile += n_clusters) {
             int tr, tc;
             tile_at(a, tile, tr, tc);
-            const int c = tc * 2 * CB + (int)rank * CB + q * 32 + lane;
-            const bool cv = c < a.C;
+            const int c0 = tc * 2 * CB + (int)rank * CB;
             const long long r0 = (long long)tr * a.bn;
             const int rows = (int)min((long long)a.bn, a.R - r0);
-            const float bias = a.epi.bias && cv ? a.epi.bias[c] : 0.f;
-            if (*abort_flag || !mbar_wait(&acc_full[acc], aph)) { *abort_flag = 1; break; }
+            const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
+            // the group leaves together: its warps meet at the staging barrier
+            if (!group_and(mbar_wait(&acc_full[acc], aph), st.bar)) { *abort_flag = 1; break; }
             tc_fence_after();
             const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
             for (int j = half * 32; j < rows; j += 64) {
                 uint32_t v[32];
                 tmem_ld32(t + j, v);
                 tc_wait_ld_regs(v);
-                epilogue32<ACT>(a.epi, v, r0 + j, rows - j, c, cv, bias);
+                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, r0 + j, rows - j, c0, cl, bias, st);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8 * acc);
             if (++acc == 2) { acc = 0; aph ^= 1; }
         }
+        if (st.tid == 0) bulk_wait<0>();
     }
     tc_fence_before();
     __syncwarp();
@@ -334,6 +422,7 @@ __host__ __device__ constexpr int sp_tmem_cols(int bn) { return bn <= 32 ? 32 : 
 template <bool AMN, bool BMN, int ACT, int PARTS>
 __global__ void __launch_bounds__(SP_THREADS)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
                     const __grid_constant__ TcArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -426,26 +515,27 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         if (elect_one()) tc_commit(acc_full);
         __syncwarp();
     } else {
-        const int q = warp & 3;
-        const int c = c0 + q * 32 + lane;
+        const int q = warp & 3, cl = q * 32 + lane;
         const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16);
-        const bool ok = mbar_wait(acc_full, 0) && !*abort_flag;
+        const bool ok = group_and(mbar_wait(acc_full, 0) && !*abort_flag, 1);
         tc_fence_after();
         if (!ok) {
             *abort_flag = 1;
         } else if (a.splits == 1) {
-            const bool cv = c < a.C;
+            // the stages are no longer needed: every copy has landed and every MMA has read it
+            Staging st{smem, 0, 1, cl};
             const int rows = (int)min((long long)a.bn, a.R - r0);
-            const float bias = a.epi.bias && cv ? a.epi.bias[c] : 0.f;
+            const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
             for (int j = 0; j < rows; j += 32) {
                 uint32_t v[32];
                 tmem_ld32(t + j, v);               // (bn = 16: the upper half is not used, the allocation has 32 columns)
                 tc_wait_ld_regs(v);
-                epilogue32<ACT>(a.epi, v, r0 + j, rows - j, c, cv, bias);
+                epilogue32<ACT>(a, &tmOut, &tmZ, v, r0 + j, min(a.bn, rows) - j, c0, cl, bias, st);
             }
+            if (cl == 0) bulk_wait<0>();
         } else {
             // row j of the tile is finished by CTA j >> per_log; it gets this CTA's partial sums of it
-            const uint32_t mine = smem_u32(red) + (uint32_t)((((rank << a.per_log) * CB) + q * 32 + lane) * 4);
+            const uint32_t mine = smem_u32(red) + (uint32_t)((((rank << a.per_log) * CB) + cl) * 4);
             for (int j0 = 0; j0 < a.bn; j0 += 32) {
                 uint32_t v[32];
                 tmem_ld32(t + j0, v);
@@ -517,6 +607,38 @@ bool operand_map(CUtensorMap* m, const void* base, int inner, int outer, long lo
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A bf16 [rows, cols] tensor that is stored in boxes of 32 rows x 128 columns.
+bool stored_map(CUtensorMap* m, void* base, int cols, int rows, long long ld)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {(cuuint32_t)CB, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What goes through shared memory, and its maps (an unused map is a copy of mA).
+bool epilogue_maps(const TcProduct& p, int bn, const CUtensorMap& mA, int& staged, CUtensorMap* mO, CUtensorMap* mZ)
+{
+    const LinEpilogue& e = p.epi;
+    staged = 0;
+    *mO = *mZ = mA;
+    if (bn < 32) return true;            // a box of 32 rows would reach into the next tile
+    if (!e.out_f32 && e.ld_out % 8 == 0) {
+        staged |= ST_OUT;
+        if (!stored_map(mO, e.out, p.C, p.R, e.ld_out)) return false;
+    }
+    if (e.z && e.ld_z % 8 == 0) {
+        staged |= ST_Z;
+        if (!stored_map(mZ, e.z, p.C, p.R, e.ld_z)) return false;
+    }
+    if (e.residual && !e.out_f32 && e.ld_r % 8 == 0 && p.C % 8 == 0) staged |= ST_RES;
+    return true;
+}
+
 struct Plan {
     int pair, bn, splits, stages, occ, group;
 };
@@ -550,7 +672,7 @@ Plan choose(const TcProduct& p)
             const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
             const double step = std::max(2.0 * bn, (A_BYTES + bn * 64) / 64.0);
             const double t = waves * (nkb * step + 300) + 5000 + 10 * bn;
-            if (t < least) { least = t; best = Plan{1, bn, 1, PR_STAGES, 1, 8}; }
+            if (t < least) { least = t; best = Plan{1, bn, 1, 0, 1, 8}; }
         }
     }
     const int tc = cdiv(p.C, CB);
@@ -574,7 +696,7 @@ Plan choose(const TcProduct& p)
 template <bool AMN, bool BMN, int ACT>
 moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
 {
-    CUtensorMap mA, mB;
+    CUtensorMap mA, mB, mO, mZ;
     TcArgs a{};
     a.R = p.R;
     a.C = p.C;
@@ -591,11 +713,13 @@ moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
         return MOE_ERR_CUDA;
     if (!(BMN ? operand_map(&mB, p.B, p.R, p.K, p.ldb, 1, 0, 64) : operand_map(&mB, p.B, p.K, p.R, p.ldb, 1, 0, pl.bn / 2)))
         return MOE_ERR_CUDA;
+    if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
+    a.stages = pr_stages((int)a.b_bytes);
     auto* fn = linear_pair_kernel<AMN, BMN, ACT>;
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), PR_SMEM);
     if (e != cudaSuccess) return cuda_status(e);
     const int clusters = (int)std::min<long long>(tiles, num_sms() / 2);
-    fn<<<2 * clusters, PR_THREADS, PR_SMEM, st>>>(mA, mB, a);
+    fn<<<2 * clusters, PR_THREADS, PR_SMEM, st>>>(mA, mB, mO, mZ, a);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
@@ -603,7 +727,7 @@ moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
 template <bool AMN, bool BMN, int ACT, int PARTS>
 moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
 {
-    CUtensorMap mA, mB;
+    CUtensorMap mA, mB, mO, mZ;
     TcArgs a{};
     a.R = p.R;
     a.C = p.C;
@@ -623,6 +747,7 @@ moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
     if (!(BMN ? operand_map(&mB, p.B, p.R, p.K, p.ldb, PARTS, p.b_plane, 64)
               : operand_map(&mB, p.B, p.K, p.R, p.ldb, PARTS, p.b_plane, pl.bn)))
         return MOE_ERR_CUDA;
+    if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
     auto* fn = linear_split_kernel<AMN, BMN, ACT, PARTS>;
     const int smem = 1024 + pl.stages * sp_stage_bytes(p, pl.bn) + (pl.splits > 1 ? pl.bn * CB * 4 : 0) + 256;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem);
@@ -637,7 +762,7 @@ moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
     at[0].val.clusterDim = {(unsigned)pl.splits, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fn, mA, mB, a);
+    e = cudaLaunchKernelEx(&cfg, fn, mA, mB, mO, mZ, a);
     count_launch();
     return e == cudaSuccess ? cuda_status(cudaGetLastError()) : MOE_ERR_CUDA;
 }
