@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
             const int c = c0 + 32 * i;
             if (c >= a.N) continue;
             float v = ld1(a.dy, (long long)m * a.ld_dy + c, a.dy_f32);
-            if (a.act != MOE_ACT_NONE) v *= act_slope(ld1(a.z, (long long)m * a.ld_z + c, a.z_f32), a.act);
+            if (a.act != MOE_ACT_NONE) v = __fmul_rn(v, act_slope(ld1(a.z, (long long)m * a.ld_z + c, a.z_f32), a.act));
             acc[i] += v;
             if (!a.dz) continue;
             const long long at = (long long)m * a.ld_dz + c;

@@ -24,15 +24,30 @@ struct LinEpilogue {
     int out_f32, z_f32;
 };
 
-// phi and Phi of the exact GELU.  erff is within 2 ulp.
-__device__ __forceinline__ float norm_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678118654752f)); }
+// Phi(-|z|), with e = exp(-z^2 / 2): half of erfc(|z| / sqrt 2) by formula
+// 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions (error of
+// erf at most 1.5e-7, so at most 0.75e-7 here).  Branch-free, and the lower
+// tail is formed without a cancellation; with erff the epilogue of a 256 x 256
+// tile took 13.9 us, longer than the tile's products up to K = 1600.
+__device__ __forceinline__ float norm_tail(float z, float e)
+{
+    const float t = __fdividef(1.0f, fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
+    const float p = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t,
+                         0.254829592f);
+    return 0.5f * e * p * t;
+}
 
+// The fast exponential and quotient (2 + 1.17 |z| and 2 steps) cost the
+// result |z| (4 + 1.2 |z|) steps of fp32 at most, far below a bf16 rounding.
 __device__ __forceinline__ float act_apply(float z, int act)
 {
     if (act == MOE_ACT_RELU) return z > 0.f || z != z ? z : 0.f;
-    // below -88 exp overflows and z / inf = -0, as it should be
-    if (act == MOE_ACT_SILU) return z == -INFINITY ? 0.f : z / (1.0f + __expf(-z));
-    if (act == MOE_ACT_GELU) return z == -INFINITY ? 0.f : z * norm_cdf(z);
+    // far below zero 1 + exp(-z) is infinite and the quotient 0
+    if (act == MOE_ACT_SILU) return z == -INFINITY ? 0.f : __fdividef(z, 1.0f + __expf(-z));
+    if (act == MOE_ACT_GELU) {
+        const float h = norm_tail(z, __expf(-0.5f * z * z));
+        return z == -INFINITY ? 0.f : z * (z < 0.f ? h : 1.0f - h);
+    }
     return z;
 }
 
@@ -42,12 +57,13 @@ __device__ __forceinline__ float act_slope(float z, int act)
     if (act == MOE_ACT_SILU) {
         if (z == -INFINITY) return 0.f;
         if (z == INFINITY) return 1.f;
-        const float s = 1.0f / (1.0f + __expf(-z));
+        const float s = __fdividef(1.0f, 1.0f + __expf(-z));
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
     if (act == MOE_ACT_GELU) {
+        const float e = __expf(-0.5f * z * z), h = norm_tail(z, e);
         if (fabsf(z) == INFINITY) return z > 0.f ? 1.f : 0.f;
-        return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), norm_cdf(z));
+        return fmaf(z * 0.39894228040143268f, e, z < 0.f ? h : 1.0f - h);
     }
     return 1.f;
 }

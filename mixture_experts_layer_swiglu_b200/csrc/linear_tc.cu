@@ -165,10 +165,22 @@ struct Staging {
     }
 };
 
+// A chunk's residual as its group holds it before the chunk is processed: four
+// 16-byte pieces per thread, loaded while the chunk before it is at work.
+__device__ __forceinline__ void residual_load(const TcArgs& a, uint4 (&res)[4], long long r0, int nr, int c0, int tid)
+{
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.epi.residual) + r0 * a.epi.ld_r + c0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = k * 8 + tid / 16, u = tid % 16;
+        if (r < nr && c0 + u * 8 < a.C) res[k] = *reinterpret_cast<const uint4*>(p + r * a.epi.ld_r + u * 8);
+    }
+}
+
 template <int ACT>
 __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* tmOut, const CUtensorMap* tmZ,
-                                           const uint32_t (&acc)[32], long long r0, int nr, int c0, int cl, float bias,
-                                           Staging& st)
+                                           const uint32_t (&acc)[32], const uint4 (&res)[4], long long r0, int nr, int c0,
+                                           int cl, float bias, Staging& st)
 {
     const LinEpilogue& e = a.epi;
     const int c = c0 + cl;
@@ -191,14 +203,9 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
     uint8_t* b = a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
     __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + cl;
     if (a.staged & ST_RES) {
-        const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(e.residual) + r0 * e.ld_r + c0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = k * 8 + st.tid / 16, u = st.tid % 16;
-            if (r < nr && c0 + u * 8 < a.C)
-                *reinterpret_cast<uint4*>(b + r * (CB * 2) + u * 16) =
-                    *reinterpret_cast<const uint4*>(res + r * e.ld_r + u * 8);
-        }
+        for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(b + (k * 8 + st.tid / 16) * (CB * 2) + (st.tid % 16) * 16) = res[k];
         st.sync();
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]) + __bfloat162float(mine[i * CB]);
@@ -385,6 +392,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             const long long r0 = (long long)tr * a.bn;
             const int rows = (int)min((long long)a.bn, a.R - r0);
             const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
+            uint4 res[4] = {};
+            if (a.staged & ST_RES) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, cl);
             // the group leaves together: its warps meet at the staging barrier
             if (!group_and(mbar_wait(&acc_full[acc], aph), st.bar)) { *abort_flag = 1; break; }
             tc_fence_after();
@@ -393,7 +402,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 uint32_t v[32];
                 tmem_ld32(t + j, v);
                 tc_wait_ld_regs(v);
-                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, r0 + j, rows - j, c0, cl, bias, st);
+                const uint4 now[4] = {res[0], res[1], res[2], res[3]};
+                if ((a.staged & ST_RES) && j + 64 < rows) residual_load(a, res, r0 + j + 64, rows - j - 64, c0, cl);
+                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, c0, cl, bias, st);
             }
             tc_fence_before();
             __syncwarp();
@@ -517,6 +528,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     } else {
         const int q = warp & 3, cl = q * 32 + lane;
         const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16);
+        uint4 res[4] = {};
+        if (a.splits == 1 && (a.staged & ST_RES))
+            residual_load(a, res, r0, (int)min((long long)a.bn, a.R - r0), c0, cl);
         const bool ok = group_and(mbar_wait(acc_full, 0) && !*abort_flag, 1);
         tc_fence_after();
         if (!ok) {
@@ -530,7 +544,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                 uint32_t v[32];
                 tmem_ld32(t + j, v);               // (bn = 16: the upper half is not used, the allocation has 32 columns)
                 tc_wait_ld_regs(v);
-                epilogue32<ACT>(a, &tmOut, &tmZ, v, r0 + j, min(a.bn, rows) - j, c0, cl, bias, st);
+                const uint4 now[4] = {res[0], res[1], res[2], res[3]};
+                if ((a.staged & ST_RES) && j + 32 < rows) residual_load(a, res, r0 + j + 32, rows - j - 32, c0, cl);
+                epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, c0, cl, bias, st);
             }
             if (cl == 0) bulk_wait<0>();
         } else {
