@@ -68,19 +68,35 @@ __device__ __forceinline__ float act_slope(float z, int act)
     return 1.f;
 }
 
-__device__ __forceinline__ void lin_store(const LinEpilogue& e, long long r, int c, float v)
+__device__ __forceinline__ float lin_residual(const LinEpilogue& e, long long r, int c)
 {
-    if (e.bias) v += e.bias[c];
+    return e.out_f32 ? static_cast<const float*>(e.residual)[r * e.ld_r + c]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[r * e.ld_r + c]);
+}
+
+// One element from its sum v, with its bias and residual at hand.
+template <int ACT>
+__device__ __forceinline__ void lin_finish(const LinEpilogue& e, long long r, int c, float v, float bias, float residual)
+{
+    v += bias;
     if (e.z) {
         if (e.z_f32) static_cast<float*>(e.z)[r * e.ld_z + c] = v;
         else static_cast<__nv_bfloat16*>(e.z)[r * e.ld_z + c] = __float2bfloat16_rn(v);
     }
-    v = act_apply(v, e.act);
-    if (e.residual)
-        v += e.out_f32 ? static_cast<const float*>(e.residual)[r * e.ld_r + c]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[r * e.ld_r + c]);
+    v = act_apply(v, ACT) + residual;
     if (e.out_f32) static_cast<float*>(e.out)[r * e.ld_out + c] = v;
     else static_cast<__nv_bfloat16*>(e.out)[r * e.ld_out + c] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ void lin_store(const LinEpilogue& e, long long r, int c, float v)
+{
+    const float bias = e.bias ? e.bias[c] : 0.f, res = e.residual ? lin_residual(e, r, c) : 0.f;
+    switch (e.act) {
+        case MOE_ACT_RELU: return lin_finish<MOE_ACT_RELU>(e, r, c, v, bias, res);
+        case MOE_ACT_SILU: return lin_finish<MOE_ACT_SILU>(e, r, c, v, bias, res);
+        case MOE_ACT_GELU: return lin_finish<MOE_ACT_GELU>(e, r, c, v, bias, res);
+        default: return lin_finish<MOE_ACT_NONE>(e, r, c, v, bias, res);
+    }
 }
 
 // fp32: out[r, c] = epi(sum_k P(r, k) Q(c, k)), element (r, k) of P at r * p_rs + k * p_ks (one of them 1), Q alike.

@@ -109,16 +109,16 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Whether `ok` holds for all 128 threads of a named barrier's group.
-__device__ __forceinline__ bool group_and(bool ok, int bar)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)ok), "r"(bar) : "memory");
-    return r != 0;
-}
+// The cluster's barrier in two halves (every thread of every CTA, once each).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// Barrier 15 over a block: one side waits, the other only arrives.
+template <int N>
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 15, %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void block_arrive() { asm volatile("bar.arrive 15, %0;" ::"n"(N) : "memory"); }
 
 template <int ACT>
 __device__ __forceinline__ float act_t(float z)
@@ -126,30 +126,29 @@ __device__ __forceinline__ float act_t(float z)
     return act_apply(z, ACT);
 }
 
-// 32 accumulator columns of this lane: rows r0 .. r0 + 31 of column c0 + cl.
+// 32 accumulator columns of this lane: rows r0 .. r0 + 31 of column c0 + lane.
 // nr: rows of them that exist; cv: the column exists.
 //
-// bf16 rows pass through shared memory: a lane's element is 2 bytes, so storing
-// it directly makes 64-byte pieces per warp (8.5 us per 256 x 256 tile, more than
-// a K = 512 tile's MMAs).  The four warps of a group (one per TMEM lane quarter)
-// lay a chunk of 32 rows x 128 columns into one of two 8 KB buffers, from which
-// one TMA store writes whole 256-byte rows and clips what lies outside the
-// tensor; a residual comes in through the same buffer by 16-byte loads.  Rows
-// that TMA cannot address (a stride that is not a multiple of 16 bytes) are
-// stored directly, and fp32 rows too (128 bytes per warp as it is).
-constexpr int STAGE_ROWS = 32 * CB * 2;
+// bf16 rows pass through shared memory: a lane's element is 2 bytes, and
+// storing it directly took 8.5 us per 256 x 256 tile, more than a K = 512 tile's
+// MMAs.  A warp lays its 32 rows x 32 columns into one of two 2 KB buffers of
+// its own, from which a TMA store writes them and clips what lies outside the
+// tensor; a residual comes in through the same buffer by 16-byte loads.  (Four
+// warps sharing 256-byte rows needed two barriers per chunk: 4.6 us per tile.)
+// Rows that TMA cannot address (a stride that is not a multiple of 16 bytes)
+// are stored directly, and fp32 rows too (128 bytes per warp as it is).
+constexpr int BOX_C = 32;
+constexpr int STAGE_ROWS = 32 * BOX_C * 2;
 struct Staging {
     uint8_t* buf;            // two buffers of STAGE_ROWS bytes
     int at;                  // the next one
-    int bar;                 // named barrier of the group's 128 threads
-    int tid;                 // thread of the group
+    int lane;
 
-    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
     // the next buffer, once the store that last used it has read it
     __device__ __forceinline__ uint8_t* acquire()
     {
-        if (tid == 0) bulk_wait_read<1>();
-        sync();
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
         uint8_t* b = buf + at * STAGE_ROWS;
         at ^= 1;
         return b;
@@ -157,22 +156,22 @@ struct Staging {
     __device__ __forceinline__ void store(const CUtensorMap* m, const uint8_t* b, int c0, int r0) const
     {
         fence_proxy_async_smem();
-        sync();
-        if (tid == 0) {
+        __syncwarp();
+        if (lane == 0) {
             tma_store_2d(m, b, c0, r0);
             bulk_commit();
         }
     }
 };
 
-// A chunk's residual as its group holds it before the chunk is processed: four
-// 16-byte pieces per thread, loaded while the chunk before it is at work.
-__device__ __forceinline__ void residual_load(const TcArgs& a, uint4 (&res)[4], long long r0, int nr, int c0, int tid)
+// A chunk's residual as its warp holds it before the chunk is processed: four
+// 16-byte pieces per lane, loaded while the chunk before it is at work.
+__device__ __forceinline__ void residual_load(const TcArgs& a, uint4 (&res)[4], long long r0, int nr, int c0, int lane)
 {
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.epi.residual) + r0 * a.epi.ld_r + c0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int r = k * 8 + tid / 16, u = tid % 16;
+        const int r = k * 8 + lane / 4, u = lane % 4;
         if (r < nr && c0 + u * 8 < a.C) res[k] = *reinterpret_cast<const uint4*>(p + r * a.epi.ld_r + u * 8);
     }
 }
@@ -180,19 +179,19 @@ __device__ __forceinline__ void residual_load(const TcArgs& a, uint4 (&res)[4], 
 template <int ACT>
 __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* tmOut, const CUtensorMap* tmZ,
                                            const uint32_t (&acc)[32], const uint4 (&res)[4], long long r0, int nr, int c0,
-                                           int cl, float bias, Staging& st)
+                                           float bias, Staging& st)
 {
     const LinEpilogue& e = a.epi;
-    const int c = c0 + cl;
+    const int c = c0 + st.lane;
     const bool cv = c < a.C;
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) + bias;
     if (a.staged & ST_Z) {
         uint8_t* b = st.acquire();
-        __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + cl;
+        __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + st.lane;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mine[i * CB] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 32; ++i) mine[i * BOX_C] = __float2bfloat16_rn(v[i]);
         st.store(tmZ, b, c0, (int)r0);
     } else if (e.z) {
         __nv_bfloat16* z = static_cast<__nv_bfloat16*>(e.z) + r0 * e.ld_z + c;
@@ -201,14 +200,14 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
             if (cv && i < nr) z[i * e.ld_z] = __float2bfloat16_rn(v[i]);
     }
     uint8_t* b = a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
-    __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + cl;
+    __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + st.lane;
     if (a.staged & ST_RES) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(b + (k * 8 + st.tid / 16) * (CB * 2) + (st.tid % 16) * 16) = res[k];
-        st.sync();
+            *reinterpret_cast<uint4*>(b + (k * 8 + st.lane / 4) * (BOX_C * 2) + (st.lane % 4) * 16) = res[k];
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]) + __bfloat162float(mine[i * CB]);
+        for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]) + __bfloat162float(mine[i * BOX_C]);
     } else if (e.residual) {
         float res[32];
         if (e.out_f32) {
@@ -228,7 +227,7 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
     }
     if (a.staged & ST_OUT) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mine[i * CB] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 32; ++i) mine[i * BOX_C] = __float2bfloat16_rn(v[i]);
         st.store(tmOut, b, c0, (int)r0);
     } else if (e.out_f32) {
         float* p = static_cast<float*>(e.out) + r0 * e.ld_out + c;
@@ -247,7 +246,7 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
 constexpr int PR_MAX_STAGES = 10;
 constexpr int PR_EPI_WARPS = 8;                                // two per TMEM lane quarter, alternate 32-row chunks
 constexpr int PR_THREADS = 64 + 32 * PR_EPI_WARPS;
-constexpr int PR_STAGING = 2 * 2 * STAGE_ROWS;                 // two groups of four warps
+constexpr int PR_STAGING = PR_EPI_WARPS * 2 * STAGE_ROWS;
 constexpr int PR_SMEM = 227 * 1024;
 // as many stages as fit: 6 of 32 KB (bn = 256) to 9 of 20 KB (bn = 64)
 __host__ __device__ constexpr int pr_stages(int b_bytes)
@@ -293,11 +292,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
     const int total = a.tiles_r * a.tiles_c;
 
-    if (threadIdx.x == 32) {
-        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 2 * PR_EPI_WARPS); }
-        mbar_init(mma_done, 1);
-        *abort_flag = 0;
+    if (warp == 0) {
+        // full, empty, acc_full, acc_empty and mma_done lie in a row: a barrier per lane
+        static_assert(2 * PR_MAX_STAGES + 5 <= 31, "");
+        const int first = 2 * PR_MAX_STAGES + 2;
+        if (lane < 2 * PR_MAX_STAGES + 5) mbar_init(full + lane, lane == first || lane == first + 1 ? 2 * PR_EPI_WARPS : 1);
+        if (lane == 31) *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) { tmem_alloc_pair(tmem_slot, 512); tmem_relinquish_pair(); }
@@ -381,21 +381,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         }
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
-        const int cl = q * 32 + lane;
-        Staging st{staging + half * 2 * STAGE_ROWS, 0, 1 + half, cl};
+        Staging st{staging + (warp - 2) * 2 * STAGE_ROWS, 0, lane};
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = cluster; tile < total; tile += n_clusters) {
             int tr, tc;
             tile_at(a, tile, tr, tc);
-            const int c0 = tc * 2 * CB + (int)rank * CB;
+            const int c0 = tc * 2 * CB + (int)rank * CB + q * 32;
             const long long r0 = (long long)tr * a.bn;
             const int rows = (int)min((long long)a.bn, a.R - r0);
-            const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
+            const float bias = a.epi.bias && c0 + lane < a.C ? a.epi.bias[c0 + lane] : 0.f;
             uint4 res[4] = {};
-            if (a.staged & ST_RES) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, cl);
-            // the group leaves together: its warps meet at the staging barrier
-            if (!group_and(mbar_wait(&acc_full[acc], aph), st.bar)) { *abort_flag = 1; break; }
+            if (a.staged & ST_RES) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, lane);
+            if (!warp_wait(&acc_full[acc], aph)) { *abort_flag = 1; break; }
             tc_fence_after();
             const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
             for (int j = half * 32; j < rows; j += 64) {
@@ -403,15 +401,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 tmem_ld32(t + j, v);
                 tc_wait_ld_regs(v);
                 const uint4 now[4] = {res[0], res[1], res[2], res[3]};
-                if ((a.staged & ST_RES) && j + 64 < rows) residual_load(a, res, r0 + j + 64, rows - j - 64, c0, cl);
-                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, c0, cl, bias, st);
+                if ((a.staged & ST_RES) && j + 64 < rows) residual_load(a, res, r0 + j + 64, rows - j - 64, c0, lane);
+                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, c0, bias, st);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8 * acc);
             if (++acc == 2) { acc = 0; aph ^= 1; }
         }
-        if (st.tid == 0) bulk_wait<0>();
+        if (lane == 0) bulk_wait_read<0>();        // the buffers are read; the writes end with the kernel
     }
     tc_fence_before();
     __syncwarp();
@@ -455,21 +453,26 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     const int kb0 = (int)((long long)a.nkb * rank / a.splits), kb1 = (int)((long long)a.nkb * (rank + 1) / a.splits);
     const int cols = sp_tmem_cols(a.bn);
 
-    if (threadIdx.x == 32) {
-        for (int s = 0; s < a.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-        mbar_init(acc_full, 1);
-        *abort_flag = 0;
+    // The producer starts its loads before the block's first barrier; the
+    // cluster's barrier is only announced here, and awaited before the first
+    // partial sum is sent: by then the peers have long started.
+    bool waited = a.splits == 1;
+    if (a.splits > 1) cluster_arrive_relaxed();
+    if (warp == 0) {
+        // (full, empty and acc_full lie in a row: a barrier per lane)
+        if (lane < 2 * SP_MAX_STAGES + 1) mbar_init(full + lane, 1);
+        if (lane == 31) *abort_flag = 0;
         fence_barrier_init();
+        __syncwarp();
+    } else {
+        if (warp == 1) { tmem_alloc(tmem_slot, cols); tmem_relinquish(); }
+        tc_fence_before();
+        block_sync<SP_THREADS>();
+        tc_fence_after();
     }
-    if (warp == 1) { tmem_alloc(tmem_slot, cols); tmem_relinquish(); }
-    if (threadIdx.x == 64) { tma_prefetch_desc(&tmA); tma_prefetch_desc(&tmB); }
-    tc_fence_before();
-    __syncthreads();
-    if (a.splits > 1) cluster_sync_all();          // the peers' shared memory exists before anything is sent there
-    tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
 
     if (warp == 0) {
+        block_arrive<SP_THREADS>();
         int s = 0;
         uint32_t ph = 0;
         bool bad = false;
@@ -503,6 +506,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             while (globaltimer() - t0 < 200000ull) { }
         }
     } else if (warp == 1) {
+        const uint32_t tmem_base = *tmem_slot;
         const uint32_t idesc = idesc_bf16_f32(CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
         const uint64_t ad0 = operand_desc<AMN>(smem), bd0 = operand_desc<BMN>(smem + A_BYTES);
         const uint32_t stage16 = stage_bytes >> 4, part16 = a.b_bytes >> 4;
@@ -526,18 +530,18 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         if (elect_one()) tc_commit(acc_full);
         __syncwarp();
     } else {
-        const int q = warp & 3, cl = q * 32 + lane;
-        const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16);
+        const int q = warp & 3, cl = q * 32 + lane, cq = c0 + q * 32;
+        const uint32_t t = *tmem_slot + ((uint32_t)(q * 32) << 16);
         uint4 res[4] = {};
         if (a.splits == 1 && (a.staged & ST_RES))
-            residual_load(a, res, r0, (int)min((long long)a.bn, a.R - r0), c0, cl);
-        const bool ok = group_and(mbar_wait(acc_full, 0) && !*abort_flag, 1);
+            residual_load(a, res, r0, (int)min((long long)a.bn, a.R - r0), cq, lane);
+        const bool ok = warp_wait(acc_full, 0) && !*abort_flag;
         tc_fence_after();
         if (!ok) {
             *abort_flag = 1;
         } else if (a.splits == 1) {
             // the stages are no longer needed: every copy has landed and every MMA has read it
-            Staging st{smem, 0, 1, cl};
+            Staging st{smem + q * 2 * STAGE_ROWS, 0, lane};
             const int rows = (int)min((long long)a.bn, a.R - r0);
             const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
             for (int j = 0; j < rows; j += 32) {
@@ -545,12 +549,14 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                 tmem_ld32(t + j, v);               // (bn = 16: the upper half is not used, the allocation has 32 columns)
                 tc_wait_ld_regs(v);
                 const uint4 now[4] = {res[0], res[1], res[2], res[3]};
-                if ((a.staged & ST_RES) && j + 32 < rows) residual_load(a, res, r0 + j + 32, rows - j - 32, c0, cl);
-                epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, c0, cl, bias, st);
+                if ((a.staged & ST_RES) && j + 32 < rows) residual_load(a, res, r0 + j + 32, rows - j - 32, cq, lane);
+                if (cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, cq, bias, st);
             }
-            if (cl == 0) bulk_wait<0>();
+            if (lane == 0) bulk_wait_read<0>();
         } else {
             // row j of the tile is finished by CTA j >> per_log; it gets this CTA's partial sums of it
+            cluster_wait();
+            waited = true;
             const uint32_t mine = smem_u32(red) + (uint32_t)((((rank << a.per_log) * CB) + cl) * 4);
             for (int j0 = 0; j0 < a.bn; j0 += 32) {
                 uint32_t v[32];
@@ -566,25 +572,41 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             }
         }
     }
+    if (!waited) cluster_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, cols);
+        tmem_dealloc(*tmem_slot, cols);
     }
     if (a.splits == 1) return;
-    cluster_sync_all();                            // every partial sum has arrived
-    const int per = 1 << a.per_log;
-    const long long rb = r0 + (long long)rank * per;
-    // a warp finishes 32 columns of a row at a time
-    for (int u = warp; u < per * (CB / 32); u += SP_THREADS / 32) {
-        const int j = u / (CB / 32), cc = (u % (CB / 32)) * 32 + lane, c = c0 + cc;
-        float v = 0.f;
-        for (int s = 0; s < a.splits; ++s) v += red[(s * per + j) * CB + cc];
-        if (rb + j < a.R && c < a.C) {
-            LinEpilogue e = a.epi;
-            e.act = ACT;
-            lin_store(e, rb + j, c, v);
+    // A warp finishes 32 columns of four rows at a time; the first four units'
+    // bias and residual are fetched under the cluster's barrier.
+    const int units = CB / 32 << a.per_log;
+    const long long rb = r0 + ((long long)rank << a.per_log);
+    float add[4], bias[4];
+    auto fetch = [&](int u0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int u = u0 + i * (SP_THREADS / 32), c = c0 + (u % 4) * 32 + lane;
+            const long long r = rb + u / 4;
+            const bool in = u < units && c < a.C && r < a.R;
+            bias[i] = in && a.epi.bias ? a.epi.bias[c] : 0.f;
+            add[i] = in && a.epi.residual ? lin_residual(a.epi, r, c) : 0.f;
+        }
+    };
+    fetch(warp);
+    cluster_arrive();
+    cluster_wait();                                // every partial sum has arrived
+    for (int u0 = warp; u0 < units; u0 += 4 * (SP_THREADS / 32)) {
+        if (u0 != warp) fetch(u0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int u = u0 + i * (SP_THREADS / 32), cc = (u % 4) * 32 + lane, j = u / 4;
+            if (u >= units) break;
+            float v = 0.f;
+            for (int s = 0; s < a.splits; ++s) v += red[((s << a.per_log) + j) * CB + cc];
+            if (rb + j < a.R && c0 + cc < a.C) lin_finish<ACT>(a.epi, rb + j, c0 + cc, v, bias[i], add[i]);
         }
     }
 }
@@ -623,14 +645,14 @@ bool operand_map(CUtensorMap* m, const void* base, int inner, int outer, long lo
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A bf16 [rows, cols] tensor that is stored in boxes of 32 rows x 128 columns.
+// A bf16 [rows, cols] tensor that is stored in boxes of 32 rows x 32 columns.
 bool stored_map(CUtensorMap* m, void* base, int cols, int rows, long long ld)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {(cuuint32_t)CB, 32};
+    cuuint32_t box[2] = {BOX_C, 32};
     cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
