@@ -43,10 +43,10 @@ struct TcArgs {
     int tiles_r, tiles_c, group_r;
     int stages, splits, per_log;                // split form; log2 of the rows that each CTA of a cluster finishes
     uint32_t b_bytes;                           // B bytes of one stage, part and CTA
-    int staged;                                 // ST_* bits: which bf16 tensors go through shared memory
+    int staged;                                 // ST_* bits: which tensors go through shared memory
     LinEpilogue epi;
 };
-constexpr int ST_OUT = 1, ST_Z = 2, ST_RES = 4;
+constexpr int ST_OUT = 1, ST_Z = 2, ST_RES = 4, ST_OUT32 = 8;
 
 // Descriptor of an MN-major tile with 128-byte swizzle: 8 steps of the
 // contraction x 64 elements are 1024 B (stride offset), the next 64 elements
@@ -135,8 +135,9 @@ __device__ __forceinline__ float act_t(float z)
 // its own, from which a TMA store writes them and clips what lies outside the
 // tensor; a residual comes in through the same buffer by 16-byte loads.  (Four
 // warps sharing 256-byte rows needed two barriers per chunk: 4.6 us per tile.)
-// Rows that TMA cannot address (a stride that is not a multiple of 16 bytes)
-// are stored directly, and fp32 rows too (128 bytes per warp as it is).
+// fp32 output rows take both buffers as one (stored directly, 32 rows took a warp
+// 1650 clocks; so, 350).  Rows that TMA cannot address (a stride that is not a
+// multiple of 16 bytes) are stored directly.
 constexpr int BOX_C = 32;
 constexpr int STAGE_ROWS = 32 * BOX_C * 2;
 struct Staging {
@@ -152,6 +153,14 @@ struct Staging {
         uint8_t* b = buf + at * STAGE_ROWS;
         at ^= 1;
         return b;
+    }
+    // both buffers
+    __device__ __forceinline__ uint8_t* acquire_all()
+    {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        at = 0;
+        return buf;
     }
     __device__ __forceinline__ void store(const CUtensorMap* m, const uint8_t* b, int c0, int r0) const
     {
@@ -199,7 +208,7 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
         for (int i = 0; i < 32; ++i)
             if (cv && i < nr) z[i * e.ld_z] = __float2bfloat16_rn(v[i]);
     }
-    uint8_t* b = a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
+    uint8_t* b = a.staged & ST_OUT32 ? st.acquire_all() : a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
     __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + st.lane;
     if (a.staged & ST_RES) {
 #pragma unroll
@@ -228,6 +237,11 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
     if (a.staged & ST_OUT) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) mine[i * BOX_C] = __float2bfloat16_rn(v[i]);
+        st.store(tmOut, b, c0, (int)r0);
+    } else if (a.staged & ST_OUT32) {
+        float* mine32 = reinterpret_cast<float*>(b) + st.lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mine32[i * BOX_C] = v[i];
         st.store(tmOut, b, c0, (int)r0);
     } else if (e.out_f32) {
         float* p = static_cast<float*>(e.out) + r0 * e.ld_out + c;
@@ -421,7 +435,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 }
 
 // ------------------------------------------------------------ split form
-constexpr int SP_THREADS = 192;
+constexpr int SP_THREADS = 192;               // (eight epilogue warps: slower by 0.4 us at every size, 96 registers each)
 constexpr int SP_MAX_STAGES = 12;
 
 __host__ __device__ constexpr int sp_tmem_cols(int bn) { return bn <= 32 ? 32 : bn <= 64 ? 64 : bn <= 128 ? 128 : 256; }
@@ -533,16 +547,15 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         const int q = warp & 3, cl = q * 32 + lane, cq = c0 + q * 32;
         const uint32_t t = *tmem_slot + ((uint32_t)(q * 32) << 16);
         uint4 res[4] = {};
-        if (a.splits == 1 && (a.staged & ST_RES))
-            residual_load(a, res, r0, (int)min((long long)a.bn, a.R - r0), cq, lane);
+        const int rows = (int)min((long long)a.bn, a.R - r0);
+        if (a.splits == 1 && (a.staged & ST_RES)) residual_load(a, res, r0, rows, cq, lane);
         const bool ok = warp_wait(acc_full, 0) && !*abort_flag;
         tc_fence_after();
         if (!ok) {
             *abort_flag = 1;
         } else if (a.splits == 1) {
             // the stages are no longer needed: every copy has landed and every MMA has read it
-            Staging st{smem + q * 2 * STAGE_ROWS, 0, lane};
-            const int rows = (int)min((long long)a.bn, a.R - r0);
+            Staging st{smem + (warp - 2) * 2 * STAGE_ROWS, 0, lane};
             const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
             for (int j = 0; j < rows; j += 32) {
                 uint32_t v[32];
@@ -645,17 +658,17 @@ bool operand_map(CUtensorMap* m, const void* base, int inner, int outer, long lo
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A bf16 [rows, cols] tensor that is stored in boxes of 32 rows x 32 columns.
-bool stored_map(CUtensorMap* m, void* base, int cols, int rows, long long ld)
+// A [rows, cols] tensor that is stored in boxes of 32 rows x 32 columns.
+bool stored_map(CUtensorMap* m, void* base, int cols, int rows, long long ld, bool f32)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
     cuuint32_t box[2] = {BOX_C, 32};
     cuuint32_t estr[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // What goes through shared memory, and its maps (an unused map is a copy of mA).
@@ -665,13 +678,13 @@ bool epilogue_maps(const TcProduct& p, int bn, const CUtensorMap& mA, int& stage
     staged = 0;
     *mO = *mZ = mA;
     if (bn < 32) return true;            // a box of 32 rows would reach into the next tile
-    if (!e.out_f32 && e.ld_out % 8 == 0) {
-        staged |= ST_OUT;
-        if (!stored_map(mO, e.out, p.C, p.R, e.ld_out)) return false;
+    if (e.ld_out % (e.out_f32 ? 4 : 8) == 0) {
+        staged |= e.out_f32 ? ST_OUT32 : ST_OUT;
+        if (!stored_map(mO, e.out, p.C, p.R, e.ld_out, e.out_f32 != 0)) return false;
     }
     if (e.z && e.ld_z % 8 == 0) {
         staged |= ST_Z;
-        if (!stored_map(mZ, e.z, p.C, p.R, e.ld_z)) return false;
+        if (!stored_map(mZ, e.z, p.C, p.R, e.ld_z, false)) return false;
     }
     if (e.residual && !e.out_f32 && e.ld_r % 8 == 0 && p.C % 8 == 0) staged |= ST_RES;
     return true;
