@@ -43,6 +43,7 @@ struct TcArgs {
     int tiles_r, tiles_c, group_r;
     int stages, splits, per_log;                // split form; log2 of the rows that each CTA of a cluster finishes
     uint32_t b_bytes;                           // B bytes of one stage, part and CTA
+    int vec4;                                   // split form: rows can be read and written four elements at a time
     int staged;                                 // ST_* bits: which tensors go through shared memory
     LinEpilogue epi;
 };
@@ -438,7 +439,65 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 constexpr int SP_THREADS = 192;               // (eight epilogue warps: slower by 0.4 us at every size, 96 registers each)
 constexpr int SP_MAX_STAGES = 12;
 
-__host__ __device__ constexpr int sp_tmem_cols(int bn) { return bn <= 32 ? 32 : bn <= 64 ? 64 : bn <= 128 ? 128 : 256; }
+__host__ __device__ constexpr int sp_tmem_cols(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+
+// Accumulator columns j .. j + 31 of this lane.  The parts of a three-part B
+// are three 64-wide boxes in a row, which one MMA takes as N = 192 (as three
+// MMAs of N <= 64 each they took 75 clocks apiece, whatever their N): their
+// accumulators are added here, the small ones first.
+template <int PARTS>
+__device__ __forceinline__ void acc_load(uint32_t t, int j, uint32_t (&v)[32])
+{
+    tmem_ld32(t + j, v);
+    if constexpr (PARTS == 3) {
+        uint32_t m[32], l[32];
+        tmem_ld32(t + 64 + j, m);
+        tmem_ld32(t + 128 + j, l);
+        tc_wait_ld_regs(l);
+        tc_wait_ld_regs(m);
+        tc_wait_ld_regs(v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(__uint_as_float(v[i]) + (__uint_as_float(m[i]) + __uint_as_float(l[i])));
+    } else {
+        tc_wait_ld_regs(v);
+    }
+}
+
+// Four neighbouring elements of a row, as one access where strides and length allow (vec).
+__device__ __forceinline__ void row4_load(const LinEpilogue& e, int vec, long long r, int c, int C, float (&v)[4])
+{
+    if (vec && c + 3 < C) {
+        if (e.out_f32) {
+            const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + r * e.ld_r + c);
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.residual) + r * e.ld_r + c);
+            v[0] = bf16_lo(x.x); v[1] = bf16_hi(x.x); v[2] = bf16_lo(x.y); v[3] = bf16_hi(x.y);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (c + i < C) v[i] = lin_residual(e, r, c + i);
+}
+
+__device__ __forceinline__ void row4_store(void* base, long long ld, int f32, int vec, long long r, int c, int C,
+                                           const float (&v)[4])
+{
+    if (vec && c + 3 < C) {
+        if (f32) *reinterpret_cast<float4*>(static_cast<float*>(base) + r * ld + c) = make_float4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + r * ld + c) =
+                 make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (c + i < C) {
+            if (f32) static_cast<float*>(base)[r * ld + c + i] = v[i];
+            else static_cast<__nv_bfloat16*>(base)[r * ld + c + i] = __float2bfloat16_rn(v[i]);
+        }
+}
 
 // Shared memory: stages x (A, then the parts of B), the partial sums that the
 // cluster's CTAs send here ([splits][bn / splits][128] fp32), the barriers.
@@ -465,7 +524,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     const int c0 = tc * CB;
     const long long r0 = (long long)tr * a.bn;
     const int kb0 = (int)((long long)a.nkb * rank / a.splits), kb1 = (int)((long long)a.nkb * (rank + 1) / a.splits);
-    const int cols = sp_tmem_cols(a.bn);
+    static_assert(PARTS == 1 || (PARTS == 3 && BMN), "three parts: 64-wide boxes");
+    const int cols = sp_tmem_cols(PARTS * a.bn);
 
     // The producer starts its loads before the block's first barrier; the
     // cluster's barrier is only announced here, and awaited before the first
@@ -521,9 +581,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         }
     } else if (warp == 1) {
         const uint32_t tmem_base = *tmem_slot;
-        const uint32_t idesc = idesc_bf16_f32(CB, a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+        const uint32_t idesc = idesc_bf16_f32(CB, PARTS * a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
         const uint64_t ad0 = operand_desc<AMN>(smem), bd0 = operand_desc<BMN>(smem + A_BYTES);
-        const uint32_t stage16 = stage_bytes >> 4, part16 = a.b_bytes >> 4;
+        const uint32_t stage16 = stage_bytes >> 4;
         int s = 0;
         uint32_t ph = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -531,11 +591,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             const uint64_t ad = ad0 + (uint64_t)(s * stage16), bd = bd0 + (uint64_t)(s * stage16);
             if (elect_one()) {
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                    for (int kk = 0; kk < KB / 16; ++kk)
-                        tc_mma_bf16(tmem_base, ad + kk * kStepDesc<AMN>, bd + p * part16 + kk * kStepDesc<BMN>, idesc,
-                                    kb > kb0 || p > 0 || kk > 0);
+                for (int kk = 0; kk < KB / 16; ++kk)
+                    tc_mma_bf16(tmem_base, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, kb > kb0 || kk > 0);
                 tc_commit(&empty[s]);
             }
             __syncwarp();
@@ -559,8 +616,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
             for (int j = 0; j < rows; j += 32) {
                 uint32_t v[32];
-                tmem_ld32(t + j, v);               // (bn = 16: the upper half is not used, the allocation has 32 columns)
-                tc_wait_ld_regs(v);
+                acc_load<PARTS>(t, j, v);          // (bn = 16: the upper half is not used, the allocation has 32 columns)
                 const uint4 now[4] = {res[0], res[1], res[2], res[3]};
                 if ((a.staged & ST_RES) && j + 32 < rows) residual_load(a, res, r0 + j + 32, rows - j - 32, cq, lane);
                 if (cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, cq, bias, st);
@@ -573,8 +629,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             const uint32_t mine = smem_u32(red) + (uint32_t)((((rank << a.per_log) * CB) + cl) * 4);
             for (int j0 = 0; j0 < a.bn; j0 += 32) {
                 uint32_t v[32];
-                tmem_ld32(t + j0, v);
-                tc_wait_ld_regs(v);
+                acc_load<PARTS>(t, j0, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int j = j0 + i;
@@ -593,34 +648,33 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         tmem_dealloc(*tmem_slot, cols);
     }
     if (a.splits == 1) return;
-    // A warp finishes 32 columns of four rows at a time; the first four units'
-    // bias and residual are fetched under the cluster's barrier.
-    const int units = CB / 32 << a.per_log;
+    // A warp finishes a row of 128 columns at a time, four per lane.  (32 columns
+    // of single elements at a time: 570 clocks each, 3.3 us for 16 rows.)
+    const int per = 1 << a.per_log, c = c0 + lane * 4;
     const long long rb = r0 + ((long long)rank << a.per_log);
-    float add[4], bias[4];
-    auto fetch = [&](int u0) {
+    float bias[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int u = u0 + i * (SP_THREADS / 32), c = c0 + (u % 4) * 32 + lane;
-            const long long r = rb + u / 4;
-            const bool in = u < units && c < a.C && r < a.R;
-            bias[i] = in && a.epi.bias ? a.epi.bias[c] : 0.f;
-            add[i] = in && a.epi.residual ? lin_residual(a.epi, r, c) : 0.f;
-        }
-    };
-    fetch(warp);
+    for (int i = 0; i < 4; ++i) bias[i] = a.epi.bias && c + i < a.C ? a.epi.bias[c + i] : 0.f;
     cluster_arrive();
     cluster_wait();                                // every partial sum has arrived
-    for (int u0 = warp; u0 < units; u0 += 4 * (SP_THREADS / 32)) {
-        if (u0 != warp) fetch(u0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int u = u0 + i * (SP_THREADS / 32), cc = (u % 4) * 32 + lane, j = u / 4;
-            if (u >= units) break;
-            float v = 0.f;
-            for (int s = 0; s < a.splits; ++s) v += red[((s << a.per_log) + j) * CB + cc];
-            if (rb + j < a.R && c0 + cc < a.C) lin_finish<ACT>(a.epi, rb + j, c0 + cc, v, bias[i], add[i]);
+    for (int j = warp; j < per; j += SP_THREADS / 32) {
+        if (rb + j >= a.R) break;
+        float res[4] = {0.f, 0.f, 0.f, 0.f}, v[4];
+        if (a.epi.residual) row4_load(a.epi, a.vec4, rb + j, c, a.C, res);
+        const float4* p = reinterpret_cast<const float4*>(red + j * CB) + lane;
+        float4 sum = p[0];
+#pragma unroll 8
+        for (int s = 1; s < a.splits; ++s) {
+            const float4 x = p[(s * CB / 4) << a.per_log];
+            sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
         }
+        const float acc[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = acc[i] + bias[i];
+        if (a.epi.z) row4_store(a.epi.z, a.epi.ld_z, 0, a.vec4, rb + j, c, a.C, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = act_t<ACT>(v[i]) + res[i];
+        row4_store(a.epi.out, a.epi.ld_out, a.epi.out_f32, a.vec4, rb + j, c, a.C, v);
     }
 }
 
@@ -707,10 +761,12 @@ int sp_stages(const TcProduct& p, int bn, int splits, int occ)
     return std::min(SP_MAX_STAGES, room / sp_stage_bytes(p, bn));
 }
 
-// Which form and tile: the smallest estimate of the SM clocks.  Per 64-wide step
-// of the contraction a CTA's MMAs take 2 bn clocks (pair: 256 x bn on two SMs,
-// split: 128 x bn on one at half of that), its loads its bytes over ~64 B per
-// clock and SM from L2.
+// Which form and tile: the smallest estimate of the time in us.  Its terms are
+// fits to measurements on a B200 (errors of 10-15%):
+//   pair   a step (64 of the contraction) 0.13 + 0.00057 bn, the rest of a launch
+//          4.1 + 0.0105 bn (set-up 1 us, first load 0.7 us, last tile's epilogue);
+//   split  a step 0.18 + 0.0004 bn with one CTA on an SM, 0.15 + 0.0024 bn with
+//          two; the rest 4.6 + 0.0065 bn, and 1 + 0.02 bn to add partial tiles.
 Plan choose(const TcProduct& p)
 {
     const int nkb = cdiv(p.K, KB), sms = num_sms();
@@ -718,26 +774,26 @@ Plan choose(const TcProduct& p)
     double least = 1e30;
     if (p.b_parts == 1) {
         const int tc = cdiv(p.C, 2 * CB);
-        for (int bn = 64; bn <= 256; bn += 32) {
+        for (int bn = 32; bn <= 256; bn += 32) {
             const long long tiles = (long long)tc * cdiv(p.R, bn);
             const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
-            const double step = std::max(2.0 * bn, (A_BYTES + bn * 64) / 64.0);
-            const double t = waves * (nkb * step + 300) + 5000 + 10 * bn;
+            const double t = waves * (nkb * (0.13 + 0.00057 * bn) + 0.3) + 4.1 + 0.0105 * bn;
             if (t < least) { least = t; best = Plan{1, bn, 1, 0, 1, 8}; }
         }
     }
     const int tc = cdiv(p.C, CB);
     for (int bn : {16, 32, 64, 128}) {
-        if (p.b_parts > 1 && bn > 64) continue;
+        if (p.b_parts > 1 && bn != 64) continue;
         const long long tiles = (long long)tc * cdiv(p.R, bn);
         for (int S = 1; S <= 8; S *= 2) {
-            if (S > nkb || bn / S < 1) continue;
+            if (S > nkb) continue;
             const int occ = sp_stages(p, bn, S, 2) >= 3 ? 2 : 1;
             const int stages = sp_stages(p, bn, S, occ);
             if (stages < 2) continue;
             const long long waves = (tiles * S + (long long)sms * occ - 1) / ((long long)sms * occ);
-            const double step = occ * std::max(2.0 * bn * p.b_parts, sp_stage_bytes(p, bn) / 64.0);
-            const double t = waves * (cdiv(nkb, S) * step + 3000 + 16 * bn + (S > 1 ? 2500 + 8 * bn : 0)) + 2000;
+            const bool two = tiles * S > sms && occ == 2;
+            const double step = two ? 0.15 + 0.0024 * bn * p.b_parts : 0.18 + 0.0004 * bn * p.b_parts;
+            const double t = waves * (cdiv(nkb, S) * step + 0.5 + 0.0065 * bn) + 4.1 + (S > 1 ? 1.0 + 0.02 * bn : 0.0);
             if (t < least) { least = t; best = Plan{0, bn, S, stages, occ, 1}; }
         }
     }
@@ -788,6 +844,7 @@ moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
     a.tiles_c = cdiv(p.C, CB);
     a.stages = pl.stages;
     a.splits = pl.splits;
+    a.vec4 = p.epi.ld_out % 4 == 0 && p.epi.ld_r % 4 == 0 && p.epi.ld_z % 4 == 0;
     while ((pl.bn >> a.per_log) > pl.splits) ++a.per_log;
     a.epi = p.epi;
     a.b_bytes = BMN ? cdiv(pl.bn, 64) * BOX_BYTES : pl.bn * 128;
