@@ -49,16 +49,16 @@ constexpr int DZ_COLS = 128;
 struct DzArgs {
     const void* dy;
     const void* z;
-    void* dz;                    // fp32, or `parts` bf16 planes
+    void* dz;                    // fp32, or `parts` bf16 matrices side by side, `step` columns apart
     float* part;
-    long long ld_dy, ld_z, ld_dz, plane;
+    long long ld_dy, ld_z, ld_dz;
     int M, N, act, rows;         // rows per range
-    int dy_f32, z_f32, dz_f32, parts;
+    int dy_f32, z_f32, dz_f32, parts, step;
 };
 
 // v as a sum of bf16 values: each part the nearest bf16 of what the parts
 // before it left (24 bits in three).  An infinity or NaN is its first part.
-__device__ __forceinline__ void store_parts(__nv_bfloat16* p, long long plane, int parts, float v)
+__device__ __forceinline__ void store_parts(__nv_bfloat16* p, int step, int parts, float v)
 {
     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
     p[0] = hi;
@@ -66,8 +66,8 @@ __device__ __forceinline__ void store_parts(__nv_bfloat16* p, long long plane, i
     const float h = __bfloat162float(hi);
     const float r1 = fabsf(h) < INFINITY ? v - h : 0.f;
     const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
-    p[plane] = mid;
-    p[2 * plane] = __float2bfloat16_rn(r1 - __bfloat162float(mid));
+    p[step] = mid;
+    p[2 * step] = __float2bfloat16_rn(r1 - __bfloat162float(mid));
 }
 
 __device__ __forceinline__ float ld1(const void* p, long long i, int f32)
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
             if (!a.dz) continue;
             const long long at = (long long)m * a.ld_dz + c;
             if (a.dz_f32) static_cast<float*>(a.dz)[at] = v;
-            else store_parts(static_cast<__nv_bfloat16*>(a.dz) + at, a.plane, a.parts, v);
+            else store_parts(static_cast<__nv_bfloat16*>(a.dz) + at, a.step, a.parts, v);
         }
     }
     if (!a.part) return;
@@ -161,7 +161,12 @@ Rows packed(const void* p, int rows, int cols, long long ld, char*& ws, cudaStre
 
 // dz needs no buffer of its own where it is dy as it stands.
 bool dz_is_dy(const Lin& l) { return l.act == MOE_ACT_NONE && l.of32 == l.f32 && (l.f32 || l.ld_y % 8 == 0); }
+// dw with grad_f32 takes a dz that is not bf16 as it stands in three parts; the
+// layout that the three-part product wants.
 int dz_parts(const Lin& l) { return l.gf32 && !l.f32 && (l.act != MOE_ACT_NONE || l.of32) ? 3 : 1; }
+
+int dz_step(const Lin& l) { return 3ll * l.N <= 64 ? l.N : (int)up8(l.N); }
+long long dz_ld(const Lin& l) { return l.f32 ? l.N : dz_parts(l) == 3 ? up8(2ll * dz_step(l) + l.N) : up8(l.N); }
 
 struct BwdLayout {
     size_t dz, part, total;
@@ -171,7 +176,7 @@ BwdLayout bwd_layout(const Lin& l)
 {
     BwdLayout b{0, 0, 0};
     int rows;
-    b.dz = dz_is_dy(l) ? 0 : al(l.f32 ? (size_t)l.M * l.N * 4 : (size_t)dz_parts(l) * l.M * up8(l.N) * 2);
+    b.dz = dz_is_dy(l) ? 0 : al((size_t)l.M * dz_ld(l) * (l.f32 ? 4 : 2));
     b.part = al((size_t)dz_chunks(l, &rows) * l.N * 4);
     b.total = b.dz + b.part + packed_bytes(l.f32, l.M, l.K, l.ld_x) + packed_bytes(l.f32, l.N, l.K, l.ld_w);
     return b;
@@ -252,7 +257,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
     float* part = reinterpret_cast<float*>(ws + b.dz);
     ws += b.dz + b.part;
     const int parts = dz_parts(l);
-    const long long ld_dz = l.f32 ? l.N : up8(l.N), plane = (long long)l.M * ld_dz;
+    const long long ld_dz = dz_ld(l);
     if (dz || db) {
         DzArgs a{};
         a.dy = dy;
@@ -261,7 +266,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         a.ld_dy = l.ld_y;
         a.ld_z = l.ld_z;
         a.ld_dz = ld_dz;
-        a.plane = plane;
+        a.step = dz_step(l);
         a.M = l.M;
         a.N = l.N;
         a.act = l.act;
@@ -296,7 +301,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
             s = launch_linear_simt(SimtProduct{static_cast<const float*>(g.p), static_cast<const float*>(x), 1, g.ld, 1, l.ld_x, l.N, l.K, l.M, epi}, st);
         } else {
             const Rows xr = packed(x, l.M, l.K, l.ld_x, ws, st);
-            s = launch_linear_tc(TcProduct{xr.p, g.p, xr.ld, g.ld, 1, 1, parts, plane, l.N, l.K, l.M, epi}, st);
+            s = launch_linear_tc(TcProduct{xr.p, g.p, xr.ld, g.ld, 1, 1, parts, dz_step(l), l.N, l.K, l.M, epi}, st);
         }
         if (s != MOE_OK) return s;
     }

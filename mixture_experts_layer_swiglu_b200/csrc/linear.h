@@ -113,14 +113,15 @@ moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st);
 // along out's contiguous dimension (C), B the other (R).  An operand is either
 // K-major (its contraction index is contiguous: element (i, k) at i * ld + k) or
 // MN-major (at k * ld + i).  Bases 16-byte aligned, ld a multiple of 8.
-//   b_parts > 1: B is the sum of that many bf16 planes, b_plane elements apart.
+//   b_parts = 3 (MN-major B only): B is the sum of three bf16 matrices that lie side
+//   by side in its rows, b_part columns apart; b_part is R while 3 R <= 64, else a
+//   multiple of 8 of at least R.
 struct TcProduct {
     const void* A;
     const void* B;
     long long lda, ldb;
     int a_mn, b_mn;
-    int b_parts;
-    long long b_plane;
+    int b_parts, b_part;
     int R, C, K;
     LinEpilogue epi;
 };

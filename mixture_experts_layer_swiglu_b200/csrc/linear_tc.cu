@@ -42,7 +42,8 @@ struct TcArgs {
     int R, C, nkb, bn;
     int tiles_r, tiles_c, group_r;
     int stages, splits, per_log;                // split form; log2 of the rows that each CTA of a cluster finishes
-    uint32_t b_bytes;                           // B bytes of one stage, part and CTA
+    uint32_t a_bytes, b_bytes;                  // bytes of one stage and CTA (split form; pair: a_bytes is A_BYTES)
+    int part, boxes, acc_part;                  // three-part B: column distance of the parts, boxes per stage, accumulator distance
     int vec4;                                   // split form: rows can be read and written four elements at a time
     int staged;                                 // ST_* bits: which tensors go through shared memory
     LinEpilogue epi;
@@ -70,24 +71,6 @@ __device__ __forceinline__ uint64_t operand_desc(const void* p)
 }
 template <bool MN>
 constexpr uint32_t kStepDesc = MN ? 2048u >> 4 : 32u >> 4;     // 16 elements of the contraction
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar_cluster, int c0, int c1,
-                                                 int c2)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
 
 // The producer and the MMA issuer are whole warps in uniform control flow, one
 // elected lane of which issues: the tensor-core and TMA instructions take their
@@ -128,7 +111,7 @@ __device__ __forceinline__ float act_t(float z)
 }
 
 // 32 accumulator columns of this lane: rows r0 .. r0 + 31 of column c0 + lane.
-// nr: rows of them that exist; cv: the column exists.
+// nr: rows that exist from r0 on; the warp's next chunk starts `next` rows on.
 //
 // bf16 rows pass through shared memory: a lane's element is 2 bytes, and
 // storing it directly took 8.5 us per 256 x 256 tile, more than a K = 512 tile's
@@ -175,9 +158,18 @@ struct Staging {
 };
 
 // A chunk's residual as its warp holds it before the chunk is processed: four
-// 16-byte pieces per lane, loaded while the chunk before it is at work.
-__device__ __forceinline__ void residual_load(const TcArgs& a, uint4 (&res)[4], long long r0, int nr, int c0, int lane)
+// (fp32: eight) 16-byte pieces per lane, loaded while the chunk before it is at work.
+__device__ __forceinline__ void residual_load(const TcArgs& a, uint4 (&res)[8], long long r0, int nr, int c0, int lane)
 {
+    if (a.epi.out_f32) {
+        const float* p = static_cast<const float*>(a.epi.residual) + r0 * a.epi.ld_r + c0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = k * 4 + lane / 8, u = lane % 8;
+            if (r < nr && c0 + u * 4 < a.C) res[k] = *reinterpret_cast<const uint4*>(p + r * a.epi.ld_r + u * 4);
+        }
+        return;
+    }
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.epi.residual) + r0 * a.epi.ld_r + c0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -188,7 +180,7 @@ __device__ __forceinline__ void residual_load(const TcArgs& a, uint4 (&res)[4], 
 
 template <int ACT>
 __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* tmOut, const CUtensorMap* tmZ,
-                                           const uint32_t (&acc)[32], const uint4 (&res)[4], long long r0, int nr, int c0,
+                                           const uint32_t (&acc)[32], uint4 (&res)[8], long long r0, int nr, int next, int c0,
                                            float bias, Staging& st)
 {
     const LinEpilogue& e = a.epi;
@@ -209,12 +201,22 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
         for (int i = 0; i < 32; ++i)
             if (cv && i < nr) z[i * e.ld_z] = __float2bfloat16_rn(v[i]);
     }
-    uint8_t* b = a.staged & ST_OUT32 ? st.acquire_all() : a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
+    uint8_t* b = a.staged & (ST_OUT | ST_OUT32 | ST_RES) && e.out_f32 ? st.acquire_all() : a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
     __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + st.lane;
-    if (a.staged & ST_RES) {
+    if ((a.staged & ST_RES) && e.out_f32) {
+        const float* mine32 = reinterpret_cast<const float*>(b) + st.lane;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(b + (k * 4 + st.lane / 8) * (BOX_C * 4) + (st.lane % 8) * 16) = res[k];
+        if (nr > next) residual_load(a, res, r0 + next, nr - next, c0, st.lane);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]) + mine32[i * BOX_C];
+    } else if (a.staged & ST_RES) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             *reinterpret_cast<uint4*>(b + (k * 8 + st.lane / 4) * (BOX_C * 2) + (st.lane % 4) * 16) = res[k];
+        if (nr > next) residual_load(a, res, r0 + next, nr - next, c0, st.lane);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = act_t<ACT>(v[i]) + __bfloat162float(mine[i * BOX_C]);
@@ -348,10 +350,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                         tma_load_2d_pair(pa, &tmA, bar, kb * KB, c0);
                     }
                     if constexpr (BMN) {
-                        tma_load_3d_pair(pb, &tmB, bar, r0, kb * KB, 0);
-                        if (bh > 64) tma_load_3d_pair(pb + BOX_BYTES, &tmB, bar, r0 + 64, kb * KB, 0);
+                        tma_load_2d_pair(pb, &tmB, bar, r0, kb * KB);
+                        if (bh > 64) tma_load_2d_pair(pb + BOX_BYTES, &tmB, bar, r0 + 64, kb * KB);
                     } else {
-                        tma_load_3d_pair(pb, &tmB, bar, kb * KB, r0, 0);
+                        tma_load_2d_pair(pb, &tmB, bar, kb * KB, r0);
                     }
                 }
                 __syncwarp();
@@ -406,7 +408,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             const long long r0 = (long long)tr * a.bn;
             const int rows = (int)min((long long)a.bn, a.R - r0);
             const float bias = a.epi.bias && c0 + lane < a.C ? a.epi.bias[c0 + lane] : 0.f;
-            uint4 res[4] = {};
+            uint4 res[8] = {};
             if (a.staged & ST_RES) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, lane);
             if (!warp_wait(&acc_full[acc], aph)) { *abort_flag = 1; break; }
             tc_fence_after();
@@ -415,9 +417,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 uint32_t v[32];
                 tmem_ld32(t + j, v);
                 tc_wait_ld_regs(v);
-                const uint4 now[4] = {res[0], res[1], res[2], res[3]};
-                if ((a.staged & ST_RES) && j + 64 < rows) residual_load(a, res, r0 + j + 64, rows - j - 64, c0, lane);
-                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, c0, bias, st);
+                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 64, c0, bias, st);
             }
             tc_fence_before();
             __syncwarp();
@@ -442,17 +442,18 @@ constexpr int SP_MAX_STAGES = 12;
 __host__ __device__ constexpr int sp_tmem_cols(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
 
 // Accumulator columns j .. j + 31 of this lane.  The parts of a three-part B
-// are three 64-wide boxes in a row, which one MMA takes as N = 192 (as three
-// MMAs of N <= 64 each they took 75 clocks apiece, whatever their N): their
-// accumulators are added here, the small ones first.
+// enter one MMA side by side, as three 64-wide boxes (N = 192) or, while the
+// three together have at most 64 columns, as one (as three MMAs they took 75
+// clocks apiece, whatever their N): their accumulators are added here, the
+// small ones first.
 template <int PARTS>
-__device__ __forceinline__ void acc_load(uint32_t t, int j, uint32_t (&v)[32])
+__device__ __forceinline__ void acc_load(uint32_t t, int j, int part, uint32_t (&v)[32])
 {
     tmem_ld32(t + j, v);
     if constexpr (PARTS == 3) {
         uint32_t m[32], l[32];
-        tmem_ld32(t + 64 + j, m);
-        tmem_ld32(t + 128 + j, l);
+        tmem_ld32(t + part + j, m);
+        tmem_ld32(t + 2 * part + j, l);
         tc_wait_ld_regs(l);
         tc_wait_ld_regs(m);
         tc_wait_ld_regs(v);
@@ -502,7 +503,7 @@ __device__ __forceinline__ void row4_store(void* base, long long ld, int f32, in
 // Shared memory: stages x (A, then the parts of B), the partial sums that the
 // cluster's CTAs send here ([splits][bn / splits][128] fp32), the barriers.
 template <bool AMN, bool BMN, int ACT, int PARTS>
-__global__ void __launch_bounds__(SP_THREADS)
+__global__ void __launch_bounds__(SP_THREADS, 2)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
                     const __grid_constant__ TcArgs a)
@@ -510,8 +511,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    const uint32_t stage_bytes = A_BYTES + PARTS * a.b_bytes;
-    float* red = reinterpret_cast<float*>(smem + (size_t)a.stages * stage_bytes);
+    const uint32_t stage_bytes = a.a_bytes + a.b_bytes;
+    float* red = reinterpret_cast<float*>(smem + (size_t)a.stages * stage_bytes +
+                                          (stage_bytes < A_BYTES ? A_BYTES - stage_bytes : 0));
     uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + (a.splits > 1 ? a.bn * CB * 4 : 0));
     uint64_t* empty = full + SP_MAX_STAGES;
     uint64_t* acc_full = empty + SP_MAX_STAGES;
@@ -525,7 +527,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     const long long r0 = (long long)tr * a.bn;
     const int kb0 = (int)((long long)a.nkb * rank / a.splits), kb1 = (int)((long long)a.nkb * (rank + 1) / a.splits);
     static_assert(PARTS == 1 || (PARTS == 3 && BMN), "three parts: 64-wide boxes");
-    const int cols = sp_tmem_cols(PARTS * a.bn);
+    const int cols = PARTS == 3 ? 256 : sp_tmem_cols(a.bn);
 
     // The producer starts its loads before the block's first barrier; the
     // cluster's barrier is only announced here, and awaited before the first
@@ -555,21 +557,21 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], stage_bytes);
                 uint8_t* pa = smem + (size_t)s * stage_bytes;
-                uint8_t* pb = pa + A_BYTES;
+                uint8_t* pb = pa + a.a_bytes;
                 if constexpr (AMN) {
                     tma_load_2d(pa, &tmA, &full[s], c0, kb * KB);
                     tma_load_2d(pa + BOX_BYTES, &tmA, &full[s], c0 + 64, kb * KB);
                 } else {
                     tma_load_2d(pa, &tmA, &full[s], kb * KB, c0);
                 }
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p, pb += a.b_bytes) {
-                    if constexpr (BMN) {
-                        for (int h = 0; h < a.bn; h += 64)
-                            tma_load_3d(pb + h * (BOX_BYTES / 64), &tmB, &full[s], (int)r0 + h, kb * KB, p);
-                    } else {
-                        tma_load_3d(pb, &tmB, &full[s], kb * KB, (int)r0, p);
-                    }
+                if constexpr (PARTS == 3) {
+                    for (int i = 0; i < a.boxes; ++i)
+                        tma_load_2d(pb + i * BOX_BYTES, &tmB, &full[s], (int)r0 + i * a.part, kb * KB);
+                } else if constexpr (BMN) {
+                    for (int h = 0; h < a.bn; h += 64)
+                        tma_load_2d(pb + h * (BOX_BYTES / 64), &tmB, &full[s], (int)r0 + h, kb * KB);
+                } else {
+                    tma_load_2d(pb, &tmB, &full[s], kb * KB, (int)r0);
                 }
             }
             __syncwarp();
@@ -581,8 +583,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         }
     } else if (warp == 1) {
         const uint32_t tmem_base = *tmem_slot;
-        const uint32_t idesc = idesc_bf16_f32(CB, PARTS * a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
-        const uint64_t ad0 = operand_desc<AMN>(smem), bd0 = operand_desc<BMN>(smem + A_BYTES);
+        const uint32_t idesc = idesc_bf16_f32(CB, PARTS == 3 ? 64 * a.boxes : a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+        const uint64_t ad0 = operand_desc<AMN>(smem), bd0 = operand_desc<BMN>(smem + a.a_bytes);
         const uint32_t stage16 = stage_bytes >> 4;
         int s = 0;
         uint32_t ph = 0;
@@ -603,7 +605,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     } else {
         const int q = warp & 3, cl = q * 32 + lane, cq = c0 + q * 32;
         const uint32_t t = *tmem_slot + ((uint32_t)(q * 32) << 16);
-        uint4 res[4] = {};
+        uint4 res[8] = {};
         const int rows = (int)min((long long)a.bn, a.R - r0);
         if (a.splits == 1 && (a.staged & ST_RES)) residual_load(a, res, r0, rows, cq, lane);
         const bool ok = warp_wait(acc_full, 0) && !*abort_flag;
@@ -616,10 +618,8 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
             for (int j = 0; j < rows; j += 32) {
                 uint32_t v[32];
-                acc_load<PARTS>(t, j, v);          // (bn = 16: the upper half is not used, the allocation has 32 columns)
-                const uint4 now[4] = {res[0], res[1], res[2], res[3]};
-                if ((a.staged & ST_RES) && j + 32 < rows) residual_load(a, res, r0 + j + 32, rows - j - 32, cq, lane);
-                if (cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, now, r0 + j, rows - j, cq, bias, st);
+                acc_load<PARTS>(t, j, a.acc_part, v);          // (bn = 16: the upper half is not used, the allocation has 32 columns)
+                if (cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 32, cq, bias, st);
             }
             if (lane == 0) bulk_wait_read<0>();
         } else {
@@ -629,7 +629,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             const uint32_t mine = smem_u32(red) + (uint32_t)((((rank << a.per_log) * CB) + cl) * 4);
             for (int j0 = 0; j0 < a.bn; j0 += 32) {
                 uint32_t v[32];
-                acc_load<PARTS>(t, j0, v);
+                acc_load<PARTS>(t, j0, a.acc_part, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int j = j0 + i;
@@ -697,17 +697,16 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// An operand as [planes][outer][inner] with 128-byte swizzled boxes of 64 x box_outer.
-bool operand_map(CUtensorMap* m, const void* base, int inner, int outer, long long ld, int planes, long long plane,
-                 int box_outer)
+// An operand as [outer][inner] with 128-byte swizzled boxes of 64 x box_outer.
+bool operand_map(CUtensorMap* m, const void* base, long long inner, int outer, long long ld, int box_outer)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes};
-    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(planes > 1 ? plane : ld * outer) * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)box_outer, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -740,7 +739,8 @@ bool epilogue_maps(const TcProduct& p, int bn, const CUtensorMap& mA, int& stage
         staged |= ST_Z;
         if (!stored_map(mZ, e.z, p.C, p.R, e.ld_z, false)) return false;
     }
-    if (e.residual && !e.out_f32 && e.ld_r % 8 == 0 && p.C % 8 == 0) staged |= ST_RES;
+    const int piece = e.out_f32 ? 4 : 8;
+    if (e.residual && e.ld_r % piece == 0 && p.C % piece == 0) staged |= ST_RES;
     return true;
 }
 
@@ -748,17 +748,30 @@ struct Plan {
     int pair, bn, splits, stages, occ, group;
 };
 
-int sp_stage_bytes(const TcProduct& p, int bn)
+// A K-major A of fewer than 128 rows (a router's weights) takes only their
+// bytes; the MMA's further rows are whatever follows in shared memory, and their
+// accumulators are not read.  16384 x 20 x 2048 in 128 blocks: 7 stages of the
+// tall operand in flight become 11.
+int sp_a_bytes(const TcProduct& p) { return p.a_mn ? A_BYTES : std::min(CB, (p.C + 7) / 8 * 8) * 128; }
+int sp_boxes(const TcProduct& p) { return 3 * p.R <= 64 ? 1 : 3; }
+int sp_b_bytes(const TcProduct& p, int bn)
 {
-    const int b = p.b_mn ? cdiv(bn, 64) * BOX_BYTES : bn * 128;
-    return A_BYTES + p.b_parts * b;
+    return p.b_parts == 3 ? sp_boxes(p) * BOX_BYTES : p.b_mn ? cdiv(bn, 64) * BOX_BYTES : bn * 128;
+}
+int sp_stage_bytes(const TcProduct& p, int bn) { return sp_a_bytes(p) + sp_b_bytes(p, bn); }
+
+// Shared memory of a split-form block besides its stages.  (The MMA of the last
+// stage reads A_BYTES from the stage's start, also where the stage is shorter.)
+int sp_other_bytes(const TcProduct& p, int bn, int splits)
+{
+    return 1024 + std::max(0, A_BYTES - sp_stage_bytes(p, bn)) + (splits > 1 ? bn * CB * 4 : 0) + 256;
 }
 
-// Shared memory of a split-form block with `occ` blocks per SM; 0 stages if it does not fit.
+// Stages of a split-form block when `occ` blocks share an SM (0: does not fit).
 int sp_stages(const TcProduct& p, int bn, int splits, int occ)
 {
-    const int room = (occ == 2 ? 113 : 226) * 1024 - 1024 - 512 - (splits > 1 ? bn * CB * 4 : 0);
-    return std::min(SP_MAX_STAGES, room / sp_stage_bytes(p, bn));
+    const int room = (occ == 2 ? 113 : 227) * 1024 - sp_other_bytes(p, bn, splits);
+    return std::max(0, std::min(SP_MAX_STAGES, room / sp_stage_bytes(p, bn)));
 }
 
 // Which form and tile: the smallest estimate of the time in us.  Its terms are
@@ -766,7 +779,9 @@ int sp_stages(const TcProduct& p, int bn, int splits, int occ)
 //   pair   a step (64 of the contraction) 0.13 + 0.00057 bn, the rest of a launch
 //          4.1 + 0.0105 bn (set-up 1 us, first load 0.7 us, last tile's epilogue);
 //   split  a step 0.18 + 0.0004 bn with one CTA on an SM, 0.15 + 0.0024 bn with
-//          two; the rest 4.6 + 0.0065 bn, and 1 + 0.02 bn to add partial tiles.
+//          two, and at least a loaded memory latency over the stages in flight;
+//          at least the loads of all tiles at 13 TB/s, the most that L2 gave;
+//          the rest 4.6 + 0.0065 bn, and 1 + 0.02 bn to add partial tiles.
 Plan choose(const TcProduct& p)
 {
     const int nkb = cdiv(p.K, KB), sms = num_sms();
@@ -787,13 +802,16 @@ Plan choose(const TcProduct& p)
         const long long tiles = (long long)tc * cdiv(p.R, bn);
         for (int S = 1; S <= 8; S *= 2) {
             if (S > nkb) continue;
-            const int occ = sp_stages(p, bn, S, 2) >= 3 ? 2 : 1;
+            const int slots = S == 8 ? sms * 13 / 16 : S == 4 ? sms * 8 / 9 : sms;     // whole clusters within the GPCs
+            const int occ = tiles * S > slots && sp_stages(p, bn, S, 2) >= 3 ? 2 : 1;
             const int stages = sp_stages(p, bn, S, occ);
             if (stages < 2) continue;
-            const long long waves = (tiles * S + (long long)sms * occ - 1) / ((long long)sms * occ);
-            const bool two = tiles * S > sms && occ == 2;
-            const double step = two ? 0.15 + 0.0024 * bn * p.b_parts : 0.18 + 0.0004 * bn * p.b_parts;
-            const double t = waves * (cdiv(nkb, S) * step + 0.5 + 0.0065 * bn) + 4.1 + (S > 1 ? 1.0 + 0.02 * bn : 0.0);
+            const long long waves = (tiles * S + (long long)slots * occ - 1) / ((long long)slots * occ);
+            const int n = p.b_parts == 3 ? 64 * sp_boxes(p) : bn;
+            const double step = std::max(occ == 2 ? 0.15 + 0.0024 * n : 0.18 + 0.0004 * n, 1.5 / stages);
+            const double loads = (double)tiles * nkb * sp_stage_bytes(p, bn) / 13e6;
+            const double t = std::max(waves * (cdiv(nkb, S) * step + 0.5 + 0.0065 * bn), loads) + 4.1 +
+                             (S > 1 ? 1.0 + 0.02 * bn : 0.0);
             if (t < least) { least = t; best = Plan{0, bn, S, stages, occ, 1}; }
         }
     }
@@ -813,12 +831,13 @@ moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
     a.tiles_c = cdiv(p.C, 2 * CB);
     a.group_r = pl.group;
     a.epi = p.epi;
+    a.a_bytes = A_BYTES;
     a.b_bytes = BMN ? cdiv(pl.bn / 2, 64) * BOX_BYTES : pl.bn / 2 * 128;
     const long long tiles = (long long)a.tiles_r * a.tiles_c;
     if (tiles >= (1ll << 30)) return MOE_ERR_UNSUPPORTED;
-    if (!(AMN ? operand_map(&mA, p.A, p.C, p.K, p.lda, 0, 0, 64) : operand_map(&mA, p.A, p.K, p.C, p.lda, 0, 0, CB)))
+    if (!(AMN ? operand_map(&mA, p.A, p.C, p.K, p.lda, 64) : operand_map(&mA, p.A, p.K, p.C, p.lda, CB)))
         return MOE_ERR_CUDA;
-    if (!(BMN ? operand_map(&mB, p.B, p.R, p.K, p.ldb, 1, 0, 64) : operand_map(&mB, p.B, p.K, p.R, p.ldb, 1, 0, pl.bn / 2)))
+    if (!(BMN ? operand_map(&mB, p.B, p.R, p.K, p.ldb, 64) : operand_map(&mB, p.B, p.K, p.R, p.ldb, pl.bn / 2)))
         return MOE_ERR_CUDA;
     if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
     a.stages = pr_stages((int)a.b_bytes);
@@ -847,17 +866,21 @@ moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
     a.vec4 = p.epi.ld_out % 4 == 0 && p.epi.ld_r % 4 == 0 && p.epi.ld_z % 4 == 0;
     while ((pl.bn >> a.per_log) > pl.splits) ++a.per_log;
     a.epi = p.epi;
-    a.b_bytes = BMN ? cdiv(pl.bn, 64) * BOX_BYTES : pl.bn * 128;
+    a.a_bytes = sp_a_bytes(p);
+    a.b_bytes = sp_b_bytes(p, pl.bn);
+    a.part = p.b_part;
+    a.boxes = PARTS == 3 ? sp_boxes(p) : 0;
+    a.acc_part = a.boxes == 1 ? p.b_part : 64;
     const long long ctas = (long long)a.tiles_r * a.tiles_c * pl.splits;
     if (ctas >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
-    if (!(AMN ? operand_map(&mA, p.A, p.C, p.K, p.lda, 0, 0, 64) : operand_map(&mA, p.A, p.K, p.C, p.lda, 0, 0, CB)))
+    if (!(AMN ? operand_map(&mA, p.A, p.C, p.K, p.lda, 64) : operand_map(&mA, p.A, p.K, p.C, p.lda, (int)a.a_bytes / 128)))
         return MOE_ERR_CUDA;
-    if (!(BMN ? operand_map(&mB, p.B, p.R, p.K, p.ldb, PARTS, p.b_plane, 64)
-              : operand_map(&mB, p.B, p.K, p.R, p.ldb, PARTS, p.b_plane, pl.bn)))
+    const long long width = PARTS == 3 ? 2ll * p.b_part + p.R : p.R;      // the parts side by side
+    if (!(BMN ? operand_map(&mB, p.B, width, p.K, p.ldb, 64) : operand_map(&mB, p.B, p.K, p.R, p.ldb, pl.bn)))
         return MOE_ERR_CUDA;
     if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
     auto* fn = linear_split_kernel<AMN, BMN, ACT, PARTS>;
-    const int smem = 1024 + pl.stages * sp_stage_bytes(p, pl.bn) + (pl.splits > 1 ? pl.bn * CB * 4 : 0) + 256;
+    const int smem = pl.stages * sp_stage_bytes(p, pl.bn) + sp_other_bytes(p, pl.bn, pl.splits);
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchConfig_t cfg{};
