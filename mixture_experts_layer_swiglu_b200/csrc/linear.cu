@@ -40,11 +40,17 @@ moe_status read_desc(const moe_linear_desc* d, Lin& l)
 
 // ------------------------------------------------------------ dz and db
 // dz = dy act'(z) (written unless dz is null) and the column sums of the
-// unrounded dz.  A block covers 128 columns of a range of rows: a lane holds
-// four columns, the warps take rows in turn; the block's sums go to part
-// [chunks, N] (or straight to db when there is one range).
+// unrounded dz, in one pass bound by memory.  A block covers COLS columns of a
+// range of rows; the block's sums go to part [chunks, N], or straight to db when
+// there is one range.  Two layouts:
+//   vec   rows of 16-byte pieces: a lane holds 8 neighbouring columns, a warp 256
+//         columns of a row, four rows in flight per warp (8192 x 4096 with SiLU:
+//         47 us, 4.3 TB/s);
+//   plain any stride and width: a lane holds one column; below 32 columns a warp
+//         takes 2 or 4 rows at once.
 constexpr int DZ_THREADS = 256;
-constexpr int DZ_COLS = 128;
+constexpr int DZ_WARPS = DZ_THREADS / 32;
+constexpr int DZ_ROWS = 4;                   // rows in flight per warp
 
 struct DzArgs {
     const void* dy;
@@ -53,7 +59,7 @@ struct DzArgs {
     float* part;
     long long ld_dy, ld_z, ld_dz;
     int M, N, act, rows;         // rows per range
-    int dy_f32, z_f32, dz_f32, parts, step;
+    int parts, step, lanes;      // lanes: columns of a warp in the plain layout (8, 16 or 32)
 };
 
 // v as a sum of bf16 values: each part the nearest bf16 of what the parts
@@ -70,61 +76,182 @@ __device__ __forceinline__ void store_parts(__nv_bfloat16* p, int step, int part
     p[2 * step] = __float2bfloat16_rn(r1 - __bfloat162float(mid));
 }
 
-__device__ __forceinline__ float ld1(const void* p, long long i, int f32)
+template <typename T>
+__device__ __forceinline__ float ld1(const T* p)
 {
-    return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+    if constexpr (sizeof(T) == 2) return __bfloat162float(*p);
+    else return *p;
 }
 
-__global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
+template <typename T>
+__device__ __forceinline__ void ld8(const T* p, float (&v)[8])
 {
-    __shared__ float s[DZ_THREADS / 32][DZ_COLS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c0 = blockIdx.x * DZ_COLS + lane;
-    const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int m = m0 + warp; m < m1; m += DZ_THREADS / 32) {
+    if constexpr (sizeof(T) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + 32 * i;
-            if (c >= a.N) continue;
-            float v = ld1(a.dy, (long long)m * a.ld_dy + c, a.dy_f32);
-            if (a.act != MOE_ACT_NONE) v = __fmul_rn(v, act_slope(ld1(a.z, (long long)m * a.ld_z + c, a.z_f32), a.act));
-            acc[i] += v;
-            if (!a.dz) continue;
-            const long long at = (long long)m * a.ld_dz + c;
-            if (a.dz_f32) static_cast<float*>(a.dz)[at] = v;
-            else store_parts(static_cast<__nv_bfloat16*>(a.dz) + at, a.step, a.parts, v);
+        for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(w[i]); v[2 * i + 1] = bf16_hi(w[i]); }
+    } else {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// (one rounding to fp32 whether or not dz is also written, so that db has the same bits either way)
+template <int ACT>
+__device__ __forceinline__ float dz_of(float dy, float z)
+{
+    if constexpr (ACT == MOE_ACT_NONE) return dy;
+    else return __fmul_rn(dy, act_slope(z, ACT));
+}
+
+// TY: type of dy; TZ: type of z and dz
+template <typename TY, typename TZ, int ACT>
+__global__ void __launch_bounds__(DZ_THREADS) linear_dz_vec_kernel(const DzArgs a)
+{
+    __shared__ float s[DZ_WARPS][256 + 8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 256 + lane * 8;
+    const long long m0 = (long long)blockIdx.y * a.rows;
+    const long long m1 = min((long long)a.M, m0 + a.rows);
+    const TY* dy = static_cast<const TY*>(a.dy) + c;
+    const TZ* z = static_cast<const TZ*>(a.z) + c;
+    float acc[8] = {};
+    if (c < a.N) {
+        for (long long m = m0 + warp; m < m1; m += DZ_WARPS * DZ_ROWS) {
+            float v[DZ_ROWS][8], zz[DZ_ROWS][8];
+#pragma unroll
+            for (int r = 0; r < DZ_ROWS; ++r)
+                if (m + r * DZ_WARPS < m1) {
+                    ld8(dy + (m + r * DZ_WARPS) * a.ld_dy, v[r]);
+                    if (ACT != MOE_ACT_NONE) ld8(z + (m + r * DZ_WARPS) * a.ld_z, zz[r]);
+                }
+#pragma unroll
+            for (int r = 0; r < DZ_ROWS; ++r) {
+                if (m + r * DZ_WARPS >= m1) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[r][i] = dz_of<ACT>(v[r][i], zz[r][i]);
+                    acc[i] += v[r][i];
+                }
+                if (!a.dz) continue;
+                const long long at = (m + r * DZ_WARPS) * a.ld_dz + c;
+                if constexpr (sizeof(TZ) == 4) {
+                    float* o = static_cast<float*>(a.dz) + at;
+                    *reinterpret_cast<float4*>(o) = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+                    *reinterpret_cast<float4*>(o + 4) = make_float4(v[r][4], v[r][5], v[r][6], v[r][7]);
+                } else {
+                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dz) + at;
+                    if (a.parts == 1)
+                        *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[r][0], v[r][1]), pack_bf16(v[r][2], v[r][3]),
+                                                                  pack_bf16(v[r][4], v[r][5]), pack_bf16(v[r][6], v[r][7]));
+                    else
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) store_parts(o + i, a.step, a.parts, v[r][i]);
+                }
+            }
         }
     }
     if (!a.part) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[warp][lane + 32 * i] = acc[i];
+    for (int i = 0; i < 8; ++i) s[warp][lane * 8 + i] = acc[i];
     __syncthreads();
-    const int c = blockIdx.x * DZ_COLS + threadIdx.x;
-    if (threadIdx.x < DZ_COLS && c < a.N) {
-        float v = 0.f;
-        for (int w = 0; w < DZ_THREADS / 32; ++w) v += s[w][threadIdx.x];
-        a.part[(long long)blockIdx.y * a.N + c] = v;
-    }
+    const int cc = blockIdx.x * 256 + threadIdx.x;
+    if (cc >= a.N) return;
+    float v = 0.f;
+    for (int w = 0; w < DZ_WARPS; ++w) v += s[w][threadIdx.x];
+    a.part[(long long)blockIdx.y * a.N + cc] = v;
 }
 
-__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int chunks, int N, float* db)
+template <typename TY, typename TZ, int ACT>
+__global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
 {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= N) return;
+    __shared__ float s[DZ_THREADS];
+    const int sub = threadIdx.x / a.lanes, subs = DZ_THREADS / a.lanes;      // rows side by side in the block
+    const int c = blockIdx.x * a.lanes + threadIdx.x % a.lanes;
+    const long long m0 = (long long)blockIdx.y * a.rows;
+    const long long m1 = min((long long)a.M, m0 + a.rows);
+    float acc = 0.f;
+    if (c < a.N) {
+        for (long long m = m0 + sub; m < m1; m += (long long)subs * DZ_ROWS) {
+            float v[DZ_ROWS], zz[DZ_ROWS];
+#pragma unroll
+            for (int r = 0; r < DZ_ROWS; ++r)
+                if (m + r * subs < m1) {
+                    v[r] = ld1(static_cast<const TY*>(a.dy) + (m + r * subs) * a.ld_dy + c);
+                    if (ACT != MOE_ACT_NONE) zz[r] = ld1(static_cast<const TZ*>(a.z) + (m + r * subs) * a.ld_z + c);
+                }
+#pragma unroll
+            for (int r = 0; r < DZ_ROWS; ++r) {
+                if (m + r * subs >= m1) break;
+                v[r] = dz_of<ACT>(v[r], zz[r]);
+                acc += v[r];
+                if (!a.dz) continue;
+                const long long at = (m + r * subs) * a.ld_dz + c;
+                if constexpr (sizeof(TZ) == 4) static_cast<float*>(a.dz)[at] = v[r];
+                else store_parts(static_cast<__nv_bfloat16*>(a.dz) + at, a.step, a.parts, v[r]);
+            }
+        }
+    }
+    if (!a.part) return;
+    s[threadIdx.x] = acc;
+    __syncthreads();
+    if (threadIdx.x >= a.lanes || c >= a.N) return;
     float v = 0.f;
+    for (int i = 0; i < subs; ++i) v += s[i * a.lanes + threadIdx.x];
+    a.part[(long long)blockIdx.y * a.N + c] = v;
+}
+
+// The ranges' sums: 32 columns per block, the warps take the ranges in turn.
+__global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, int chunks, int N, float* db)
+{
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float v = 0.f;
+    if (c < N)
 #pragma unroll 8
-    for (int i = 0; i < chunks; ++i) v += part[(long long)i * N + c];
+        for (int i = warp; i < chunks; i += 32) v += part[(long long)i * N + c];
+    s[warp][lane] = v;
+    __syncthreads();
+    if (warp > 0 || c >= N) return;
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) v += s[w][lane];
     db[c] = v;
 }
 
-// Ranges of rows of the dz pass: about four blocks per SM, at least 32 rows each.
-int dz_chunks(const Lin& l, int* rows)
+// Columns of a block, and the ranges of rows: about four blocks per SM, at
+// least 32 rows each, at most 256 ranges (their sums are added by one block).
+bool dz_vec(const Lin& l, long long ld_dz)
 {
-    const int slices = cdiv(l.N, DZ_COLS);
-    int chunks = std::max(1, std::min(cdiv(l.M, 32), cdiv(4 * 148, slices)));
+    return l.N % 8 == 0 && l.N >= 128 && l.ld_y % 8 == 0 && ld_dz % 8 == 0 && (l.act == MOE_ACT_NONE || l.ld_z % 8 == 0);
+}
+int dz_lanes(const Lin& l) { return l.N <= 8 ? 8 : l.N <= 16 ? 16 : 32; }
+int dz_chunks(const Lin& l, bool vec, int* rows)
+{
+    const int slices = cdiv(l.N, vec ? 256 : dz_lanes(l));
+    const int chunks = std::max(1, std::min(std::min(cdiv(l.M, 32), 256), cdiv(4 * 148, slices)));
     *rows = cdiv(std::max(l.M, 1), chunks);
     return cdiv(std::max(l.M, 1), *rows);
+}
+
+template <typename TY, typename TZ, int ACT>
+void launch_dz_t(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
+{
+    if (vec) linear_dz_vec_kernel<TY, TZ, ACT><<<dim3(cdiv(a.N, 256), chunks), DZ_THREADS, 0, st>>>(a);
+    else linear_dz_kernel<TY, TZ, ACT><<<dim3(cdiv(a.N, a.lanes), chunks), DZ_THREADS, 0, st>>>(a);
+}
+
+template <typename TY, typename TZ>
+void launch_dz(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
+{
+    switch (a.act) {
+        case MOE_ACT_RELU: return launch_dz_t<TY, TZ, MOE_ACT_RELU>(a, vec, chunks, st);
+        case MOE_ACT_SILU: return launch_dz_t<TY, TZ, MOE_ACT_SILU>(a, vec, chunks, st);
+        case MOE_ACT_GELU: return launch_dz_t<TY, TZ, MOE_ACT_GELU>(a, vec, chunks, st);
+        default: return launch_dz_t<TY, TZ, MOE_ACT_NONE>(a, vec, chunks, st);
+    }
 }
 
 // ------------------------------------------------------------ packed rows
@@ -175,9 +302,8 @@ struct BwdLayout {
 BwdLayout bwd_layout(const Lin& l)
 {
     BwdLayout b{0, 0, 0};
-    int rows;
     b.dz = dz_is_dy(l) ? 0 : al((size_t)l.M * dz_ld(l) * (l.f32 ? 4 : 2));
-    b.part = al((size_t)dz_chunks(l, &rows) * l.N * 4);
+    b.part = al((size_t)256 * l.N * 4);
     b.total = b.dz + b.part + packed_bytes(l.f32, l.M, l.K, l.ld_x) + packed_bytes(l.f32, l.N, l.K, l.ld_w);
     return b;
 }
@@ -270,16 +396,17 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         a.M = l.M;
         a.N = l.N;
         a.act = l.act;
-        a.dy_f32 = l.of32;
-        a.z_f32 = l.f32;
-        a.dz_f32 = l.f32;
         a.parts = dw ? parts : 1;
-        const int chunks = dz_chunks(l, &a.rows);
+        a.lanes = dz_lanes(l);
+        const bool vec = dz_vec(l, ld_dz);
+        const int chunks = dz_chunks(l, vec, &a.rows);
         a.part = db ? (chunks == 1 ? db : part) : nullptr;
-        linear_dz_kernel<<<dim3(cdiv(l.N, DZ_COLS), chunks), DZ_THREADS, 0, st>>>(a);
+        if (l.f32) launch_dz<float, float>(a, vec, chunks, st);
+        else if (l.of32) launch_dz<float, __nv_bfloat16>(a, vec, chunks, st);
+        else launch_dz<__nv_bfloat16, __nv_bfloat16>(a, vec, chunks, st);
         count_launch();
         if (db && chunks > 1) {
-            linear_db_kernel<<<cdiv(l.N, 256), 256, 0, st>>>(part, chunks, l.N, db);
+            linear_db_kernel<<<cdiv(l.N, 32), 1024, 0, st>>>(part, chunks, l.N, db);
             count_launch();
         }
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
