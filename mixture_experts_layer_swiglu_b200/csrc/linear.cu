@@ -44,13 +44,13 @@ moe_status read_desc(const moe_linear_desc* d, Lin& l)
 // range of rows; the block's sums go to part [chunks, N], or straight to db when
 // there is one range.  Two layouts:
 //   vec   rows of 16-byte pieces: a lane holds 8 neighbouring columns, a warp 256
-//         columns of a row, four rows in flight per warp (8192 x 4096 with SiLU:
-//         47 us, 4.3 TB/s);
+//         columns of a row (8192 x 4096, db alone: 26 us with ReLU, 38 us with
+//         SiLU, whose slope then takes the time);
 //   plain any stride and width: a lane holds one column; below 32 columns a warp
 //         takes 2 or 4 rows at once.
 constexpr int DZ_THREADS = 256;
 constexpr int DZ_WARPS = DZ_THREADS / 32;
-constexpr int DZ_ROWS = 4;                   // rows in flight per warp
+constexpr int DZ_ROWS = 2;                   // rows in flight per warp; with 32 warps per SM (4 rows, 16 warps: 48 us)
 
 struct DzArgs {
     const void* dy;
@@ -83,21 +83,6 @@ __device__ __forceinline__ float ld1(const T* p)
     else return *p;
 }
 
-template <typename T>
-__device__ __forceinline__ void ld8(const T* p, float (&v)[8])
-{
-    if constexpr (sizeof(T) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(w[i]); v[2 * i + 1] = bf16_hi(w[i]); }
-    } else {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-}
-
 // (one rounding to fp32 whether or not dz is also written, so that db has the same bits either way)
 template <int ACT>
 __device__ __forceinline__ float dz_of(float dy, float z)
@@ -106,9 +91,66 @@ __device__ __forceinline__ float dz_of(float dy, float z)
     else return __fmul_rn(dy, act_slope(z, ACT));
 }
 
+template <typename T>
+__device__ __forceinline__ void st8(T* p, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// Eight pieces of 16 bytes as they lie in memory, so that DZ_ROWS rows of two
+// tensors wait in few registers.
+template <typename T>
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+        if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+        else return i & 1 ? bf16_hi(u[i >> 1]) : bf16_lo(u[i >> 1]);
+    }
+};
+
+// One row's piece: dz, its sums and its rounding.
+template <typename TZ, int ACT, typename RY, typename RZ>
+__device__ __forceinline__ void dz_row(const DzArgs& a, const RY& y, const RZ& z, long long at, float (&acc)[8])
+{
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = dz_of<ACT>(y.get(i), z.get(i));
+        acc[i] += v[i];
+    }
+    if (!a.dz) return;
+    TZ* o = static_cast<TZ*>(a.dz) + at;
+    st8(o, v);
+    if constexpr (sizeof(TZ) == 2) {
+        if (a.parts == 1) return;
+        float mid[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float h = __bfloat162float(__float2bfloat16_rn(v[i]));
+            mid[i] = fabsf(h) < INFINITY ? v[i] - h : 0.f;
+            lo[i] = mid[i] - __bfloat162float(__float2bfloat16_rn(mid[i]));
+        }
+        st8(o + a.step, mid);
+        st8(o + 2 * a.step, lo);
+    }
+}
+
 // TY: type of dy; TZ: type of z and dz
 template <typename TY, typename TZ, int ACT>
-__global__ void __launch_bounds__(DZ_THREADS) linear_dz_vec_kernel(const DzArgs a)
+__global__ void __launch_bounds__(DZ_THREADS, 4) linear_dz_vec_kernel(const DzArgs a)
 {
     __shared__ float s[DZ_WARPS][256 + 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -119,38 +161,24 @@ __global__ void __launch_bounds__(DZ_THREADS) linear_dz_vec_kernel(const DzArgs 
     const TZ* z = static_cast<const TZ*>(a.z) + c;
     float acc[8] = {};
     if (c < a.N) {
-        for (long long m = m0 + warp; m < m1; m += DZ_WARPS * DZ_ROWS) {
-            float v[DZ_ROWS][8], zz[DZ_ROWS][8];
-#pragma unroll
-            for (int r = 0; r < DZ_ROWS; ++r)
-                if (m + r * DZ_WARPS < m1) {
-                    ld8(dy + (m + r * DZ_WARPS) * a.ld_dy, v[r]);
-                    if (ACT != MOE_ACT_NONE) ld8(z + (m + r * DZ_WARPS) * a.ld_z, zz[r]);
-                }
+        long long m = m0 + warp;
+        for (; m + (DZ_ROWS - 1) * DZ_WARPS < m1; m += DZ_WARPS * DZ_ROWS) {
+            Raw8<TY> y[DZ_ROWS];
+            Raw8<TZ> zz[DZ_ROWS];
 #pragma unroll
             for (int r = 0; r < DZ_ROWS; ++r) {
-                if (m + r * DZ_WARPS >= m1) break;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[r][i] = dz_of<ACT>(v[r][i], zz[r][i]);
-                    acc[i] += v[r][i];
-                }
-                if (!a.dz) continue;
-                const long long at = (m + r * DZ_WARPS) * a.ld_dz + c;
-                if constexpr (sizeof(TZ) == 4) {
-                    float* o = static_cast<float*>(a.dz) + at;
-                    *reinterpret_cast<float4*>(o) = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
-                    *reinterpret_cast<float4*>(o + 4) = make_float4(v[r][4], v[r][5], v[r][6], v[r][7]);
-                } else {
-                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dz) + at;
-                    if (a.parts == 1)
-                        *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[r][0], v[r][1]), pack_bf16(v[r][2], v[r][3]),
-                                                                  pack_bf16(v[r][4], v[r][5]), pack_bf16(v[r][6], v[r][7]));
-                    else
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) store_parts(o + i, a.step, a.parts, v[r][i]);
-                }
+                y[r].load(dy + (m + r * DZ_WARPS) * a.ld_dy);
+                if (ACT != MOE_ACT_NONE) zz[r].load(z + (m + r * DZ_WARPS) * a.ld_z);
             }
+#pragma unroll
+            for (int r = 0; r < DZ_ROWS; ++r) dz_row<TZ, ACT>(a, y[r], zz[r], (m + r * DZ_WARPS) * a.ld_dz + c, acc);
+        }
+        for (; m < m1; m += DZ_WARPS) {
+            Raw8<TY> y;
+            Raw8<TZ> zz;
+            y.load(dy + m * a.ld_dy);
+            if (ACT != MOE_ACT_NONE) zz.load(z + m * a.ld_z);
+            dz_row<TZ, ACT>(a, y, zz, m * a.ld_dz + c, acc);
         }
     }
     if (!a.part) return;

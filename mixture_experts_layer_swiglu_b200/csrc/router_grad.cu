@@ -21,7 +21,7 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kMaxE = 256;                   // router rows of the SwiGLU kind
 
-// Sum / maximum over the L lanes of a token's group (L a power of two).
+// Sum over a group of L lanes (L a power of two).
 template <int L>
 __device__ __forceinline__ float group_sum(float v)
 {
@@ -29,18 +29,6 @@ __device__ __forceinline__ float group_sum(float v)
     for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     return v;
 }
-template <int L>
-__device__ __forceinline__ float group_max(float v)
-{
-    // a NaN must survive: fmaxf drops it
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) {
-        const float u = __shfl_xor_sync(FULL, v, o);
-        v = (u > v || u != u) ? u : v;
-    }
-    return v;
-}
-
 // ------------------------------------------------------------ balance loss
 struct LossArgs {
     const float* logits;
@@ -56,99 +44,163 @@ struct LossArgs {
     int T, E, k, blocks, tokens_per_block;
 };
 
-constexpr int LOSS_THREADS = 512;
+constexpr int LOSS_THREADS = 1024;
 constexpr int LOSS_WARPS = LOSS_THREADS / 32;
+constexpr int LOSS_CLUSTER = 8;
 
-// Softmax of one token whose logits lie e = l + L * i in the group's lanes.
-// A row of -inf only has p = 0 and lse = 0.
-template <int L, int EPL>
-__device__ __forceinline__ void softmax_row(float (&z)[EPL], float& lse)
+// A token is a group of L lanes, each with EPL of its logits.  V4: the logits of
+// a lane come in fours (rows of a multiple of 4, EPL a multiple of 4), so that a
+// row of 256 is two 16-byte loads per lane instead of eight of 4 bytes.
+template <int L, int EPL, bool V4>
+__device__ __forceinline__ int expert_of(int l, int i)
 {
-    float m = z[0];
+    return V4 ? (i / 4) * (4 * L) + 4 * l + i % 4 : l + L * i;
+}
+
+template <int L, int EPL, bool V4>
+__device__ __forceinline__ void row_load(const float* row, int l, int E, bool live, float (&z)[EPL])
+{
+    if constexpr (V4) {
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) m = (z[i] > m || z[i] != z[i]) ? z[i] : m;
-    m = group_max<L>(m);
-    const bool none = m == -INFINITY;
-    float s = 0.f;
+        for (int i = 0; i < EPL; i += 4) {
+            const int e = expert_of<L, EPL, V4>(l, i);
+            float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (live && e < E) x = *reinterpret_cast<const float4*>(row + e);
+            z[i] = x.x; z[i + 1] = x.y; z[i + 2] = x.z; z[i + 3] = x.w;
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        z[i] = none ? 0.f : __expf(z[i] - m);
-        s += z[i];
+        for (int i = 0; i < EPL; ++i) z[i] = live && l + L * i < E ? row[l + L * i] : -INFINITY;
     }
-    s = group_sum<L>(s);
-    const float inv = none ? 0.f : 1.0f / s;
+}
+
+// Softmax of N tokens at once (their shuffles overlap): z becomes p.
+// A row of -inf only has p = 0 and lse = 0.
+template <int L, int EPL, int N>
+__device__ __forceinline__ void softmax_rows(float (&z)[N][EPL], float (&lse)[N])
+{
+    float m[N], s[N];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) z[i] *= inv;
-    lse = none ? 0.f : m + __logf(s);
+    for (int t = 0; t < N; ++t) {
+        m[t] = z[t][0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) m[t] = fmaxf(m[t], z[t][i]);
+    }
+    // (fmaxf drops a NaN; it comes back through exp and the sum)
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int t = 0; t < N; ++t) m[t] = fmaxf(m[t], __shfl_xor_sync(FULL, m[t], o));
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        // exp(z - m) with the row's maximum; a row of -inf only: exp(-inf - 0) = 0
+        const float c = m[t] == -INFINITY ? 0.f : m[t];
+        s[t] = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            z[t][i] = __expf(z[t][i] - c);
+            s[t] += z[t][i];
+        }
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int t = 0; t < N; ++t) s[t] += __shfl_xor_sync(FULL, s[t], o);
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        const bool none = s[t] == 0.f;
+        const float inv = none ? 0.f : __fdividef(1.0f, s[t]);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) z[t][i] *= inv;
+        lse[t] = none ? 0.f : m[t] + __logf(s[t]);
+    }
 }
 
 // The totals -> the outputs, by one block: sp [E] probability sums, sc [E + 1] counts, z the lse^2 sum.
 __device__ void loss_finish(const LossArgs& a, const float* sp, const int32_t* sc, double zsum)
 {
     __shared__ double s_red[LOSS_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = sc[a.E];
     const double inv = n > 0 ? 1.0 / n : 0.0;
     double v = 0.0;
-    for (int e = threadIdx.x; e < a.E; e += LOSS_THREADS) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         const double pm = sp[e] * inv;
         a.prob_mean[e] = (float)pm;
         a.counts[e] = sc[e];
-        v += pm * (sc[e] * inv / a.k) * (a.weight ? a.weight[e] : 1.0);
+        v += pm * (a.weight ? sc[e] * (double)a.weight[e] : (double)sc[e]);
     }
     if (threadIdx.x == 0) a.counts[a.E] = n;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+    if (lane == 0) s_red[warp] = v;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double t = 0.0;
-        for (int w = 0; w < LOSS_WARPS; ++w) t += s_red[w];
-        a.losses[0] = (float)(t * a.E);
+    if (warp > 0) return;
+    v = lane < blockDim.x / 32 && lane * 32 < a.E ? s_red[lane] : 0.0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    if (lane == 0) {
+        a.losses[0] = (float)(v * inv * a.E / a.k);
         a.losses[1] = (float)(zsum * inv);
     }
 }
 
-// One pass over the logits.  A token is a group of L lanes (L = 8, 16 or 32),
-// each lane EPL of its E logits; a lane keeps the probability sums of its
-// experts in registers over all tokens of its warp, so memory sees each logit
-// once and nothing else but E sums per block.
-template <int L, int EPL>
+// One pass over the logits.  A lane keeps the probability sums of its experts
+// in registers over all tokens of its warp, two tokens at a time, so memory sees
+// each logit once and E sums per block.
+template <int L, int EPL, bool V4>
 __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossArgs a)
 {
     __shared__ float s_p[LOSS_WARPS][kMaxE];
     __shared__ int32_t s_c[kMaxE + 1];
     __shared__ float s_z[LOSS_WARPS];
-    constexpr int G = 32 / L;                       // tokens per warp and step
+    constexpr int G = 32 / L;                       // tokens side by side in a warp
+    constexpr int N = 2;                            // and one after another
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int l = lane % L, grp = lane / L;
+    const int l = lane % L, grp = lane / L, warps = blockDim.x / 32;
     const long long t0 = (long long)blockIdx.x * a.tokens_per_block;
-    const int nt = (int)min((long long)a.tokens_per_block, a.T - t0);
-    for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) s_c[e] = 0;
+    const int nt = (int)max(0ll, min((long long)a.tokens_per_block, a.T - t0));
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) s_c[e] = 0;
     __syncthreads();
-    // counts: the block's slots one by one
-    const long long s0 = t0 * a.k;
-    for (int s = threadIdx.x; s < nt * a.k; s += LOSS_THREADS) {
-        if (a.mask && a.mask[t0 + s / a.k] == 0) continue;
-        const int e = a.idx[s0 + s];
-        if (e < 0 || e >= a.E) set_status(MOE_ERR_DEVICE_BOUNDS);
-        else atomicAdd(&s_c[e], 1);
-    }
     float acc[EPL], zacc = 0.f;
     int live_n = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
-    for (int t = warp * G; t < nt; t += LOSS_WARPS * G) {
-        const int tt = t + grp;
-        const bool live = tt < nt && (!a.mask || a.mask[t0 + tt] != 0);
-        const float* row = a.logits + (t0 + tt) * a.E;
-        float z[EPL], lse;
+    // the next tokens' logits are on their way while these are at work
+    float nz[N][EPL];
+    bool nlive[N];
+    auto fetch = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) z[i] = live && l + L * i < a.E ? __ldg(row + l + L * i) : -INFINITY;
-        softmax_row<L, EPL>(z, lse);
+        for (int u = 0; u < N; ++u) {
+            const int tt = t + grp + u * warps * G;
+            nlive[u] = tt < nt && (!a.mask || a.mask[t0 + tt] != 0);
+            row_load<L, EPL, V4>(a.logits + (t0 + tt) * a.E, l, a.E, nlive[u], nz[u]);
+        }
+    };
+    fetch(warp * G);
+    for (int t = warp * G; t < nt; t += warps * G * N) {
+        float z[N][EPL], lse[N];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) acc[i] += z[i];
-        zacc += lse * lse;
-        live_n += live;
+        for (int u = 0; u < N; ++u) {
+            live_n += nlive[u];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) z[u][i] = nz[u][i];
+        }
+        fetch(t + warps * G * N);
+        softmax_rows<L, EPL, N>(z, lse);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) acc[i] += z[u][i];
+            zacc += lse[u] * lse[u];
+        }
+    }
+    // the block's slots
+    for (int s = threadIdx.x; s < nt * a.k; s += blockDim.x) {
+        if (a.mask && a.mask[t0 + s / a.k] == 0) continue;
+        const int e = a.idx[t0 * a.k + s];
+        if (e < 0 || e >= a.E) set_status(MOE_ERR_DEVICE_BOUNDS);
+        else atomicAdd(&s_c[e], 1);
     }
     // the groups of a warp, then the warps in order
 #pragma unroll
@@ -160,67 +212,102 @@ __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossAr
     }
     if (grp == 0)
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (l + L * i < a.E) s_p[warp][l + L * i] = acc[i];
+        for (int i = 0; i < EPL; ++i) {
+            const int e = expert_of<L, EPL, V4>(l, i);
+            if (e < a.E) s_p[warp][e] = acc[i];
+        }
     if (lane == 0) {
         s_z[warp] = zacc;
         atomicAdd(&s_c[a.E], live_n);
     }
     __syncthreads();
     const bool alone = a.blocks == 1;
-    for (int e = threadIdx.x; e < a.E; e += LOSS_THREADS) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float v = 0.f;
-        for (int w = 0; w < LOSS_WARPS; ++w) v += s_p[w][e];
+        for (int w = 0; w < warps; ++w) v += s_p[w][e];
         if (alone) s_p[0][e] = v;
         else a.part_p[(long long)blockIdx.x * a.E + e] = v;
     }
     float zs = 0.f;
-    for (int w = 0; w < LOSS_WARPS; ++w) zs += s_z[w];
+    for (int w = 0; w < warps; ++w) zs += s_z[w];
     if (alone) {
         __syncthreads();
         loss_finish(a, s_p[0], s_c, zs);
         return;
     }
-    for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) a.part_c[(long long)blockIdx.x * (a.E + 1) + e] = s_c[e];
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.part_c[(long long)blockIdx.x * (a.E + 1) + e] = s_c[e];
     if (threadIdx.x == 0) a.part_z[blockIdx.x] = zs;
 }
 
-// The blocks' sums in order of blocks (one block).
-__global__ void __launch_bounds__(LOSS_THREADS) balance_loss_finish_kernel(const LossArgs a)
+// The blocks' sums: one cluster, each of its blocks a range of them (all loads
+// of a warp's rows at once), then their sums in order of rank.  (One block alone
+// took 38 us for 296 x 256 sums.)
+__global__ void __cluster_dims__(LOSS_CLUSTER, 1, 1) __launch_bounds__(LOSS_THREADS)
+balance_loss_finish_kernel(const LossArgs a)
 {
     __shared__ float s_p[LOSS_WARPS][kMaxE];
+    __shared__ float s_sum[kMaxE];
     __shared__ int32_t s_c[kMaxE + 1];
-    __shared__ double s_z[LOSS_WARPS];
+    __shared__ int32_t s_cnt[kMaxE + 1];
+    __shared__ double s_z;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b0 = (int)((long long)a.blocks * rank / LOSS_CLUSTER), b1 = (int)((long long)a.blocks * (rank + 1) / LOSS_CLUSTER);
     for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) s_c[e] = 0;
     __syncthreads();
-    // each warp the rows b = warp, warp + 16, ...
-    for (int e = lane; e <= a.E; e += 32) {
-        float p = 0.f;
-        int c = 0;
-#pragma unroll 4
-        for (int b = warp; b < a.blocks; b += LOSS_WARPS) {
-            if (e < a.E) p += a.part_p[(long long)b * a.E + e];
-            c += a.part_c[(long long)b * (a.E + 1) + e];
-        }
-        if (e < a.E) s_p[warp][e] = p;
-        atomicAdd(&s_c[e], c);
-    }
-    double z = 0.0;
-    for (int b = warp * 32 + lane; b < a.blocks; b += LOSS_THREADS) z += a.part_z[b];
+    float p[kMaxE / 32];
+    int c[kMaxE / 32 + 1];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
-    if (lane == 0) s_z[warp] = z;
+    for (int i = 0; i < kMaxE / 32; ++i) { p[i] = 0.f; c[i] = 0; }
+    c[kMaxE / 32] = 0;
+    for (int b = b0 + warp; b < b1; b += LOSS_WARPS) {
+#pragma unroll
+        for (int i = 0; i < kMaxE / 32; ++i)
+            if (lane + 32 * i < a.E) p[i] += a.part_p[(long long)b * a.E + lane + 32 * i];
+#pragma unroll
+        for (int i = 0; i <= kMaxE / 32; ++i)
+            if (lane + 32 * i <= a.E) c[i] += a.part_c[(long long)b * (a.E + 1) + lane + 32 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; ++i)
+        if (lane + 32 * i < a.E) s_p[warp][lane + 32 * i] = p[i];
+#pragma unroll
+    for (int i = 0; i <= kMaxE / 32; ++i)
+        if (lane + 32 * i <= a.E && c[i]) atomicAdd(&s_c[lane + 32 * i], c[i]);
+    if (warp == 0) {
+        double z = 0.0;
+        for (int b = b0 + lane; b < b1; b += 32) z += a.part_z[b];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
+        if (lane == 0) s_z = z;
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += LOSS_THREADS) {
         float v = 0.f;
         for (int w = 0; w < LOSS_WARPS; ++w) v += s_p[w][e];
-        s_p[0][e] = v;
+        s_sum[e] = v;
     }
-    double zs = 0.0;
-    for (int w = 0; w < LOSS_WARPS; ++w) zs += s_z[w];
-    __syncthreads();
-    loss_finish(a, s_p[0], s_c, zs);
+    cl.sync();
+    if (rank == 0) {
+        double zs = 0.0;
+        for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) {
+            float v = 0.f;
+            int n = 0;
+#pragma unroll
+            for (int r = 0; r < LOSS_CLUSTER; ++r) {
+                if (e < a.E) v += cl.map_shared_rank(s_sum, r)[e];
+                n += cl.map_shared_rank(s_c, r)[e];
+            }
+            if (e < a.E) s_p[0][e] = v;
+            s_cnt[e] = n;
+        }
+        if (threadIdx.x == 0)
+            for (int r = 0; r < LOSS_CLUSTER; ++r) zs += *cl.map_shared_rank(&s_z, r);
+        __syncthreads();
+        loss_finish(a, s_p[0], s_cnt, zs);
+    }
+    cl.sync();
 }
 
 // ------------------------------------------------------------ logit gradient
@@ -239,14 +326,17 @@ struct RouteBwdArgs {
 
 constexpr int RB_THREADS = 256;
 constexpr int RB_WARPS = RB_THREADS / 32;
+template <int EPL> constexpr int rb_tokens() { return EPL >= 8 ? 1 : 2; }    // tokens of a group at a time (registers)
 
-template <int L, int EPL>
-__global__ void __launch_bounds__(RB_THREADS) route_backward_kernel(const RouteBwdArgs a)
+// One pass: a read of the logits, a write of their gradient, and 12 bytes per
+// slot.  The gate terms are scattered into the lanes that hold the experts
+// through shared memory.
+template <int L, int EPL, bool V4>
+__global__ void __launch_bounds__(RB_THREADS, 4) route_backward_kernel(const RouteBwdArgs a)
 {
-    constexpr int G = 32 / L;
-    // the gate terms of one token, scattered by the lanes that hold its slots
-    __shared__ float s_g[RB_WARPS][G][L * EPL];
-    __shared__ uint8_t s_tag[RB_WARPS][G][L * EPL];
+    constexpr int G = 32 / L, N = rb_tokens<EPL>(), W = L * EPL;
+    __shared__ __align__(16) float s_g[RB_WARPS][G][N][W];
+    __shared__ uint8_t s_tag[RB_WARPS][G][N][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % L, grp = lane / L;
     float wf[EPL];
@@ -260,71 +350,144 @@ __global__ void __launch_bounds__(RB_THREADS) route_backward_kernel(const RouteB
         c_z = 2.0f * a.dlosses[1] * inv;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = l + L * i;
+            const int e = expert_of<L, EPL, V4>(l, i);
             if (e < a.E) wf[i] = (float)a.counts[e] * inv / (float)a.k * (a.weight ? a.weight[e] : 1.0f);
         }
     }
-    float* sg = s_g[warp][grp];
-    uint8_t* tag = s_tag[warp][grp];
-    for (int i = l; i < L * EPL; i += L) sg[i] = 0.f;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+        for (int i = l; i < W; i += L) s_g[warp][grp][u][i] = 0.f;
     __syncwarp();
-    const long long step = (long long)gridDim.x * RB_WARPS * G;
-    for (long long base = ((long long)blockIdx.x * RB_WARPS + warp) * G; base < a.T; base += step) {
-        const long long t = base + grp;
-        const bool live = t < a.T;
-        const bool counted = live && a.dlosses && (!a.mask || a.mask[t] != 0);
-        float z[EPL], d[EPL];
-        const float* row = a.logits + t * a.E;
+    const long long stride = (long long)gridDim.x * RB_WARPS * G;          // between a group's N tokens
+    // the next tokens' rows are on their way while these are at work
+    float nz[N][EPL], ng[N], ndg[N];
+    int ne[N];
+    auto fetch = [&](long long base) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) z[i] = counted && l + L * i < a.E ? row[l + L * i] : -INFINITY;
-        int e = -1;
-        float g = 0.f, dg = 0.f;
-        if (a.dgate && live && l < a.k) {
-            e = a.idx[t * a.k + l];
-            g = a.gate[t * a.k + l];
-            dg = a.dgate[t * a.k + l];
-            if (e < 0 || e >= a.E) { set_status(MOE_ERR_DEVICE_BOUNDS); e = -1; }
+        for (int u = 0; u < N; ++u) {
+            const long long t = base + grp + u * stride;
+            const bool in = t < a.T;
+            row_load<L, EPL, V4>(a.logits + t * a.E, l, a.E, in && a.dlosses && (!a.mask || a.mask[t] != 0), nz[u]);
+            ne[u] = -1;
+            ng[u] = ndg[u] = 0.f;
+            if (a.dgate && in && l < a.k) {
+                ne[u] = a.idx[t * a.k + l];
+                ng[u] = a.gate[t * a.k + l];
+                ndg[u] = a.dgate[t * a.k + l];
+            }
         }
-        if (a.dlosses) {
-            float lse, dot = 0.f;
-            softmax_row<L, EPL>(z, lse);
+    };
+    const long long first = ((long long)blockIdx.x * RB_WARPS + warp) * G;
+    fetch(first);
+    for (long long base = first; base < a.T; base += stride * N) {
+        float z[N][EPL], d[N][EPL];
+        int e[N];
+        float g[N], dg[N];
+        bool live[N];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) dot += z[i] * wf[i];
-            dot = group_sum<L>(dot);
+        for (int u = 0; u < N; ++u) {
+            live[u] = base + grp + u * stride < a.T;
+            e[u] = ne[u];
+            g[u] = ng[u];
+            dg[u] = ndg[u];
+            if (a.dgate && live[u] && l < a.k && (e[u] < 0 || e[u] >= a.E)) { set_status(MOE_ERR_DEVICE_BOUNDS); e[u] = -1; }
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) d[i] = z[i] * (c_bal * (wf[i] - dot) + c_z * lse);
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) d[i] = 0.f;
+            for (int i = 0; i < EPL; ++i) z[u][i] = nz[u][i];
         }
+        fetch(base + stride * N);
         if (a.dgate) {
-            const float mean = group_sum<L>(g * dg);
-            const float v = g * (dg - mean);
+            float mean[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) mean[u] = g[u] * dg[u];
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < N; ++u) mean[u] += __shfl_xor_sync(FULL, mean[u], o);
             // a router's ids are distinct; should two be equal (the tag of one is
             // overwritten by the other's), the slots are added one after the other
-            if (e >= 0) tag[e] = (uint8_t)l;
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                if (e[u] >= 0) s_tag[warp][grp][u][e[u]] = (uint8_t)l;
             __syncwarp();
-            const bool clash = e >= 0 && tag[e] != (uint8_t)l;
+            bool clash = false;
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                g[u] *= dg[u] - mean[u];
+                clash |= e[u] >= 0 && s_tag[warp][grp][u][e[u]] != (uint8_t)l;
+            }
             if (__any_sync(FULL, clash)) {
                 for (int j = 0; j < a.k; ++j) {
-                    if (l == j && e >= 0) sg[e] += v;
+#pragma unroll
+                    for (int u = 0; u < N; ++u)
+                        if (l == j && e[u] >= 0) s_g[warp][grp][u][e[u]] += g[u];
                     __syncwarp();
                 }
-            } else if (e >= 0) {
-                sg[e] = v;
+            } else {
+#pragma unroll
+                for (int u = 0; u < N; ++u)
+                    if (e[u] >= 0) s_g[warp][grp][u][e[u]] = g[u];
+            }
+        }
+        if (a.dlosses) {
+            float lse[N], dot[N];
+            softmax_rows<L, EPL, N>(z, lse);
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                dot[u] = 0.f;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) dot[u] += z[u][i] * wf[i];
+            }
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < N; ++u) dot[u] += __shfl_xor_sync(FULL, dot[u], o);
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) d[u][i] = z[u][i] * (c_bal * (wf[i] - dot[u]) + c_z * lse[u]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) d[u][i] = 0.f;
+        }
+        if (a.dgate) {
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                if constexpr (V4) {
+#pragma unroll
+                    for (int i = 0; i < EPL; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(&s_g[warp][grp][u][expert_of<L, EPL, V4>(l, i)]);
+                        d[u][i] += x.x; d[u][i + 1] += x.y; d[u][i + 2] += x.z; d[u][i + 3] += x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) d[u][i] += s_g[warp][grp][u][l + L * i];
+                }
             }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) d[i] += sg[l + L * i];
-            __syncwarp();
-            if (e >= 0) sg[e] = 0.f;
+            for (int u = 0; u < N; ++u)
+                if (e[u] >= 0) s_g[warp][grp][u][e[u]] = 0.f;
             __syncwarp();
         }
-        float* out = a.dlogits + t * a.E;
-        if (live)
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (l + L * i < a.E) out[l + L * i] = d[i];
+        for (int u = 0; u < N; ++u) {
+            if (!live[u]) continue;
+            float* out = a.dlogits + (base + grp + u * stride) * a.E;
+            if constexpr (V4) {
+#pragma unroll
+                for (int i = 0; i < EPL; i += 4) {
+                    const int c = expert_of<L, EPL, V4>(l, i);
+                    if (c < a.E) *reinterpret_cast<float4*>(out + c) = make_float4(d[u][i], d[u][i + 1], d[u][i + 2], d[u][i + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (l + L * i < a.E) out[l + L * i] = d[u][i];
+            }
+        }
     }
 }
 
@@ -619,26 +782,33 @@ inline bool aligned(const void* p, uintptr_t n = 16) { return (reinterpret_cast<
 inline size_t al(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 inline int router_rows(const moe_layer_desc* d) { return d->n_ffn + d->n_zero + d->n_copy + d->n_const; }
 
-// Blocks of the loss pass: one up to 1024 tokens' worth of lanes (the second
-// launch costs more than the pass), then enough tokens per block that its fixed
-// part does not count, at most two blocks per SM.
-void loss_blocks(int T, int E, int& blocks, int& per)
+// Blocks of the loss pass.  One of as many threads as two tokens per group need,
+// up to 1024 (64 groups of 32 lanes): the second launch costs more than the pass.
+// Then about four tokens per group, at most one block of 32 warps per SM.
+void loss_blocks(int T, int E, int& blocks, int& per, int& threads)
 {
     const long long lanes = (long long)T * (E <= 8 ? 8 : E <= 16 ? 16 : 32);
-    const long long want = (lanes + 8 * LOSS_THREADS - 1) / (8 * LOSS_THREADS);
-    blocks = (int)std::max<long long>(1, std::min<long long>(want, 296));
+    threads = 128;
+    while (threads < LOSS_THREADS && 2 * threads < lanes) threads *= 2;
+    const long long want = lanes <= 4 * LOSS_THREADS ? 1 : (lanes + 4 * LOSS_THREADS - 1) / (4 * LOSS_THREADS);
+    blocks = (int)std::max<long long>(1, std::min<long long>(want, num_sms()));
     per = (T + blocks - 1) / blocks;
     blocks = std::max(1, (T + per - 1) / std::max(per, 1));
 }
 
-#define MOE_LANES(E, CALL)                                 \
-    do {                                                   \
-        if ((E) <= 8) { CALL(8, 1); }                      \
-        else if ((E) <= 16) { CALL(16, 1); }               \
-        else if ((E) <= 32) { CALL(32, 1); }               \
-        else if ((E) <= 64) { CALL(32, 2); }               \
-        else if ((E) <= 128) { CALL(32, 4); }              \
-        else { CALL(32, 8); }                              \
+#define MOE_LANES(E, CALL)                                          \
+    do {                                                            \
+        if ((E) <= 8) { CALL(8, 1, false); }                        \
+        else if ((E) <= 16) { CALL(16, 1, false); }                 \
+        else if ((E) <= 32) { CALL(32, 1, false); }                 \
+        else if ((E) <= 64) { CALL(32, 2, false); }                 \
+        else if ((E) <= 128) {                                      \
+            if ((E) % 4 == 0) { CALL(32, 4, true); }                \
+            else { CALL(32, 4, false); }                            \
+        } else {                                                    \
+            if ((E) % 4 == 0) { CALL(32, 8, true); }                \
+            else { CALL(32, 8, false); }                            \
+        }                                                           \
     } while (0)
 
 }  // namespace
@@ -652,8 +822,8 @@ int64_t moe_balance_loss_workspace_size(const moe_layer_desc* d)
 {
     if (validate_desc(d) != MOE_OK || d->kind != MOE_EXPERT_SWIGLU) return -1;
     const int E = router_rows(d);
-    int blocks, per;
-    loss_blocks(d->T, E, blocks, per);
+    int blocks, per, threads;
+    loss_blocks(d->T, E, blocks, per, threads);
     return (int64_t)(al((size_t)blocks * E * 4) + al((size_t)blocks * (E + 1) * 4) + al((size_t)blocks * 4));
 }
 
@@ -682,7 +852,8 @@ moe_status moe_balance_loss(const moe_layer_desc* d, const float* logits, const 
     a.T = d->T;
     a.E = router_rows(d);
     a.k = d->top_k;
-    loss_blocks(a.T, a.E, a.blocks, a.tokens_per_block);
+    int threads;
+    loss_blocks(a.T, a.E, a.blocks, a.tokens_per_block, threads);
     char* p = static_cast<char*>(workspace);
     a.part_p = reinterpret_cast<float*>(p);
     p += al((size_t)a.blocks * a.E * 4);
@@ -690,12 +861,12 @@ moe_status moe_balance_loss(const moe_layer_desc* d, const float* logits, const 
     p += al((size_t)a.blocks * (a.E + 1) * 4);
     a.part_z = reinterpret_cast<float*>(p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define CALL(L, EPL) balance_loss_kernel<L, EPL><<<a.blocks, LOSS_THREADS, 0, st>>>(a)
+#define CALL(L, EPL, V4) balance_loss_kernel<L, EPL, V4><<<a.blocks, threads, 0, st>>>(a)
     MOE_LANES(a.E, CALL);
 #undef CALL
     count_launch();
     if (a.blocks > 1) {
-        balance_loss_finish_kernel<<<1, LOSS_THREADS, 0, st>>>(a);
+        balance_loss_finish_kernel<<<LOSS_CLUSTER, LOSS_THREADS, 0, st>>>(a);
         count_launch();
     }
     return cuda_status(cudaGetLastError());
@@ -732,9 +903,10 @@ moe_status moe_route_backward(const moe_layer_desc* d, const float* logits, cons
     a.E = router_rows(d);
     a.k = d->top_k;
     const int G = a.E <= 8 ? 4 : a.E <= 16 ? 2 : 1;
-    const int blocks = (int)std::min<long long>(((long long)a.T + RB_WARPS * G - 1) / (RB_WARPS * G), 8ll * num_sms());
+    const long long per = (long long)RB_WARPS * G * (a.E > 128 ? rb_tokens<8>() : rb_tokens<1>());
+    const int blocks = (int)std::min<long long>((a.T + per - 1) / per, 4ll * num_sms());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define CALL(L, EPL) route_backward_kernel<L, EPL><<<blocks, RB_THREADS, 0, st>>>(a)
+#define CALL(L, EPL, V4) route_backward_kernel<L, EPL, V4><<<blocks, RB_THREADS, 0, st>>>(a)
     MOE_LANES(a.E, CALL);
 #undef CALL
     count_launch();
