@@ -112,6 +112,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     }
 }
 
+// ------------------------------------------------------------ launches
+// Programmatic dependent launch: a kernel launched so starts while the kernel
+// before it in the stream drains, and touches global memory only after
+// pdl_wait(), which returns when that kernel has completed.  pdl_trigger()
+// lets the next one start early; a kernel that holds tensor memory never calls
+// it (a waiting successor on its SM could take the columns it still needs).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------ TMA
 // Untiled bulk copy of `bytes` (a multiple of 16; both addresses 16-byte
 // aligned) from global memory into this CTA's shared memory, counted on

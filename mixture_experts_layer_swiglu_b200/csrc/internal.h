@@ -19,6 +19,30 @@ int num_sms();
 cudaError_t ensure_smem_attr(const void* func, int bytes);
 moe_status validate_desc(const moe_layer_desc* d);   // the descriptor checks of every entry point
 
+// Launches `fn` with programmatic dependent launch (it must call pdl_wait()
+// before its first access to global memory), in clusters of `cluster` blocks.
+template <typename... P, typename... A>
+moe_status launch_dependent(void (*fn)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, P(args)...);
+    count_launch();
+    return e == cudaSuccess ? cuda_status(cudaGetLastError()) : MOE_ERR_CUDA;
+}
+
 // ------------------------------------------------------------ grouped GEMM
 enum EpiKind { EPI_SWIGLU = 0, EPI_BF16 = 1, EPI_F32 = 2, EPI_PK_SPLIT = 3 };
 

@@ -153,6 +153,8 @@ template <typename TY, typename TZ, int ACT>
 __global__ void __launch_bounds__(DZ_THREADS, 4) linear_dz_vec_kernel(const DzArgs a)
 {
     __shared__ float s[DZ_WARPS][256 + 8];
+    pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 256 + lane * 8;
     const long long m0 = (long long)blockIdx.y * a.rows;
@@ -196,6 +198,8 @@ template <typename TY, typename TZ, int ACT>
 __global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
 {
     __shared__ float s[DZ_THREADS];
+    pdl_wait();
+    pdl_trigger();
     const int sub = threadIdx.x / a.lanes, subs = DZ_THREADS / a.lanes;      // rows side by side in the block
     const int c = blockIdx.x * a.lanes + threadIdx.x % a.lanes;
     const long long m0 = (long long)blockIdx.y * a.rows;
@@ -235,6 +239,8 @@ __global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
 __global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, int chunks, int N, float* db)
 {
     __shared__ float s[32][33];
+    pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < N)
@@ -265,14 +271,14 @@ int dz_chunks(const Lin& l, bool vec, int* rows)
 }
 
 template <typename TY, typename TZ, int ACT>
-void launch_dz_t(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
+moe_status launch_dz_t(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
 {
-    if (vec) linear_dz_vec_kernel<TY, TZ, ACT><<<dim3(cdiv(a.N, 256), chunks), DZ_THREADS, 0, st>>>(a);
-    else linear_dz_kernel<TY, TZ, ACT><<<dim3(cdiv(a.N, a.lanes), chunks), DZ_THREADS, 0, st>>>(a);
+    return vec ? launch_dependent(linear_dz_vec_kernel<TY, TZ, ACT>, dim3(cdiv(a.N, 256), chunks), DZ_THREADS, 0, 1, st, a)
+               : launch_dependent(linear_dz_kernel<TY, TZ, ACT>, dim3(cdiv(a.N, a.lanes), chunks), DZ_THREADS, 0, 1, st, a);
 }
 
 template <typename TY, typename TZ>
-void launch_dz(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
+moe_status launch_dz(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
 {
     switch (a.act) {
         case MOE_ACT_RELU: return launch_dz_t<TY, TZ, MOE_ACT_RELU>(a, vec, chunks, st);
@@ -288,6 +294,8 @@ void launch_dz(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
 __global__ void __launch_bounds__(256) linear_pack_kernel(const __nv_bfloat16* src, long long ld_src, int rows, int cols,
                                                           __nv_bfloat16* dst, long long ld_dst)
 {
+    pdl_wait();
+    pdl_trigger();
     for (long long r = blockIdx.x; r < rows; r += gridDim.x)
         for (int c = threadIdx.x; c < cols; c += 256) dst[r * ld_dst + c] = src[r * ld_src + c];
 }
@@ -303,15 +311,15 @@ size_t packed_bytes(bool f32, long long rows, long long cols, long long ld)
 {
     return f32 || ld % 8 == 0 ? 0 : al((size_t)rows * up8(cols) * 2);
 }
-Rows packed(const void* p, int rows, int cols, long long ld, char*& ws, cudaStream_t st)
+moe_status packed(const void* p, int rows, int cols, long long ld, char*& ws, cudaStream_t st, Rows& r)
 {
-    if (ld % 8 == 0) return Rows{p, ld};
-    const Rows r{ws, up8(cols)};
-    linear_pack_kernel<<<std::min(rows, 8 * num_sms()), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(p), ld, rows, cols,
-                                                                       reinterpret_cast<__nv_bfloat16*>(ws), r.ld);
-    count_launch();
+    r = Rows{p, ld};
+    if (ld % 8 == 0) return MOE_OK;
+    r = Rows{ws, up8(cols)};
     ws += al((size_t)rows * r.ld * 2);
-    return r;
+    return launch_dependent(linear_pack_kernel, dim3(std::min(rows, 8 * num_sms())), 256, 0, 1, st,
+                            static_cast<const __nv_bfloat16*>(p), ld, rows, cols,
+                            static_cast<__nv_bfloat16*>(const_cast<void*>(r.p)), r.ld);
 }
 
 // dz needs no buffer of its own where it is dy as it stands.
@@ -380,7 +388,9 @@ moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* w, co
     const LinEpilogue epi{bias, residual, z, y, l.ld_y, l.ld_r, l.ld_z, l.act, l.of32, l.f32};
     if (!l.f32) {
         char* ws = static_cast<char*>(workspace);
-        const Rows xr = packed(x, l.M, l.K, l.ld_x, ws, st), wr = packed(w, l.N, l.K, l.ld_w, ws, st);
+        Rows xr, wr;
+        moe_status e = packed(x, l.M, l.K, l.ld_x, ws, st, xr);
+        if (e != MOE_OK || (e = packed(w, l.N, l.K, l.ld_w, ws, st, wr)) != MOE_OK) return e;
         return launch_linear_tc(TcProduct{wr.p, xr.p, wr.ld, xr.ld, 0, 0, 1, 0, l.M, l.N, l.K, epi}, st);
     }
     return launch_linear_simt(SimtProduct{static_cast<const float*>(x), static_cast<const float*>(w), l.ld_x, 1, l.ld_w, 1, l.M, l.N, l.K, epi}, st);
@@ -429,15 +439,13 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         const bool vec = dz_vec(l, ld_dz);
         const int chunks = dz_chunks(l, vec, &a.rows);
         a.part = db ? (chunks == 1 ? db : part) : nullptr;
-        if (l.f32) launch_dz<float, float>(a, vec, chunks, st);
-        else if (l.of32) launch_dz<float, __nv_bfloat16>(a, vec, chunks, st);
-        else launch_dz<__nv_bfloat16, __nv_bfloat16>(a, vec, chunks, st);
-        count_launch();
-        if (db && chunks > 1) {
-            linear_db_kernel<<<cdiv(l.N, 32), 1024, 0, st>>>(part, chunks, l.N, db);
-            count_launch();
-        }
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        s = l.f32 ? launch_dz<float, float>(a, vec, chunks, st)
+                  : l.of32 ? launch_dz<float, __nv_bfloat16>(a, vec, chunks, st)
+                           : launch_dz<__nv_bfloat16, __nv_bfloat16>(a, vec, chunks, st);
+        if (s != MOE_OK) return s;
+        if (db && chunks > 1 &&
+            (s = launch_dependent(linear_db_kernel, dim3(cdiv(l.N, 32)), 1024, 0, 1, st, part, chunks, l.N, db)) != MOE_OK)
+            return s;
     }
     const Rows g{b.dz ? dz : dy, b.dz ? ld_dz : l.ld_y};
     if (dx) {
@@ -445,7 +453,8 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         if (l.f32) {
             s = launch_linear_simt(SimtProduct{static_cast<const float*>(g.p), static_cast<const float*>(w), g.ld, 1, 1, l.ld_w, l.M, l.K, l.N, epi}, st);
         } else {
-            const Rows wr = packed(w, l.N, l.K, l.ld_w, ws, st);
+            Rows wr;
+            if ((s = packed(w, l.N, l.K, l.ld_w, ws, st, wr)) != MOE_OK) return s;
             s = launch_linear_tc(TcProduct{wr.p, g.p, wr.ld, g.ld, 1, 0, 1, 0, l.M, l.K, l.N, epi}, st);
         }
         if (s != MOE_OK) return s;
@@ -455,7 +464,8 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         if (l.f32) {
             s = launch_linear_simt(SimtProduct{static_cast<const float*>(g.p), static_cast<const float*>(x), 1, g.ld, 1, l.ld_x, l.N, l.K, l.M, epi}, st);
         } else {
-            const Rows xr = packed(x, l.M, l.K, l.ld_x, ws, st);
+            Rows xr;
+            if ((s = packed(x, l.M, l.K, l.ld_x, ws, st, xr)) != MOE_OK) return s;
             s = launch_linear_tc(TcProduct{xr.p, g.p, xr.ld, g.ld, 1, 1, parts, dz_step(l), l.N, l.K, l.M, epi}, st);
         }
         if (s != MOE_OK) return s;

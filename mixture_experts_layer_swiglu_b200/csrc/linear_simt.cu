@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProdu
     for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int j = 0; j < F; ++j) acc[i][j] = 0.f;
+    pdl_wait();
+    pdl_trigger();
     float vp[F], vq[F];
     if (kb0 < kb1) {
         fetch<TILE>(p.P, p.p_rs, p.p_ks, r0, p.R, kb0 * LS_BK, p.K, vp);
@@ -130,19 +132,7 @@ moe_status launch(const SimtProduct& p, int splits, cudaStream_t st)
     const int smem = std::max(4 * LS_BK * (TILE + 4) * 4, splits > 1 ? TILE * TILE * 4 : 0);
     auto* fn = linear_simt_kernel<TILE>;
     if (ensure_smem_attr(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return MOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * splits));
-    cfg.blockDim = dim3(LS_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)splits, 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p, splits, tiles_c);
-    count_launch();
-    return e == cudaSuccess ? cuda_status(cudaGetLastError()) : MOE_ERR_CUDA;
+    return launch_dependent(fn, dim3((unsigned)(tiles * splits)), LS_THREADS, smem, splits, st, p, splits, tiles_c);
 }
 
 }  // namespace

@@ -284,7 +284,7 @@ __device__ __forceinline__ void tile_at(const TcArgs& a, int tile, int& tr, int&
 }
 
 template <bool AMN, bool BMN, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
+__global__ void __launch_bounds__(PR_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
                    const __grid_constant__ TcArgs a)
@@ -323,6 +323,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
+    pdl_wait();
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
@@ -540,11 +541,13 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         if (lane == 31) *abort_flag = 0;
         fence_barrier_init();
         __syncwarp();
+        pdl_wait();
     } else {
         if (warp == 1) { tmem_alloc(tmem_slot, cols); tmem_relinquish(); }
         tc_fence_before();
         block_sync<SP_THREADS>();
         tc_fence_after();
+        pdl_wait();
     }
 
     if (warp == 0) {
@@ -845,9 +848,7 @@ moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), PR_SMEM);
     if (e != cudaSuccess) return cuda_status(e);
     const int clusters = (int)std::min<long long>(tiles, num_sms() / 2);
-    fn<<<2 * clusters, PR_THREADS, PR_SMEM, st>>>(mA, mB, mO, mZ, a);
-    count_launch();
-    return cuda_status(cudaGetLastError());
+    return launch_dependent(fn, dim3(2 * clusters), PR_THREADS, PR_SMEM, 2, st, mA, mB, mO, mZ, a);
 }
 
 template <bool AMN, bool BMN, int ACT, int PARTS>
@@ -881,21 +882,9 @@ moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
     if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
     auto* fn = linear_split_kernel<AMN, BMN, ACT, PARTS>;
     const int smem = pl.stages * sp_stage_bytes(p, pl.bn) + sp_other_bytes(p, pl.bn, pl.splits);
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem);
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return cuda_status(e);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(SP_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)pl.splits, 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fn, mA, mB, mO, mZ, a);
-    count_launch();
-    return e == cudaSuccess ? cuda_status(cudaGetLastError()) : MOE_ERR_CUDA;
+    return launch_dependent(fn, dim3((unsigned)ctas), SP_THREADS, smem, pl.splits, st, mA, mB, mO, mZ, a);
 }
 
 moe_status launch_plan(const TcProduct& p, const Plan& pl, cudaStream_t st)

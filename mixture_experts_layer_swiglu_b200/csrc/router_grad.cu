@@ -162,6 +162,8 @@ __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossAr
     const int nt = (int)max(0ll, min((long long)a.tokens_per_block, a.T - t0));
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) s_c[e] = 0;
     __syncthreads();
+    pdl_wait();
+    pdl_trigger();
     float acc[EPL], zacc = 0.f;
     int live_n = 0;
 #pragma unroll
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossAr
 // The blocks' sums: one cluster, each of its blocks a range of them (all loads
 // of a warp's rows at once), then their sums in order of rank.  (One block alone
 // took 38 us for 296 x 256 sums.)
-__global__ void __cluster_dims__(LOSS_CLUSTER, 1, 1) __launch_bounds__(LOSS_THREADS)
+__global__ void __launch_bounds__(LOSS_THREADS)
 balance_loss_finish_kernel(const LossArgs a)
 {
     __shared__ float s_p[LOSS_WARPS][kMaxE];
@@ -256,6 +258,8 @@ balance_loss_finish_kernel(const LossArgs a)
     const int b0 = (int)((long long)a.blocks * rank / LOSS_CLUSTER), b1 = (int)((long long)a.blocks * (rank + 1) / LOSS_CLUSTER);
     for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) s_c[e] = 0;
     __syncthreads();
+    pdl_wait();
+    pdl_trigger();
     float p[kMaxE / 32];
     int c[kMaxE / 32 + 1];
 #pragma unroll
@@ -339,6 +343,8 @@ __global__ void __launch_bounds__(RB_THREADS, 4) route_backward_kernel(const Rou
     __shared__ uint8_t s_tag[RB_WARPS][G][N][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % L, grp = lane / L;
+    pdl_wait();
+    pdl_trigger();
     float wf[EPL];
     float c_bal = 0.f, c_z = 0.f;
 #pragma unroll
@@ -568,6 +574,8 @@ __global__ void __launch_bounds__(CB_THREADS) combine_backward_kernel(const Comb
     const int vecs = a.d / 8, per = cdiv(vecs, CB_SPLIT);
     const int i0 = part * per, i1 = min(vecs, i0 + per);
     const bool want_dot = a.dgate || a.dcmix;
+    pdl_wait();
+    pdl_trigger();
     const TO* dy = reinterpret_cast<const TO*>(a.dy);
     const T* x = reinterpret_cast<const T*>(a.x);
     const T* cvec = reinterpret_cast<const T*>(a.cvec);
@@ -743,6 +751,8 @@ __global__ void __launch_bounds__(CV_THREADS) const_vec_grad_kernel(const Combin
     const long long s0 = S * rank / CV_CLUSTER, s1 = S * (rank + 1) / CV_CLUSTER;
     const TO* dy = reinterpret_cast<const TO*>(a.dy);
     float acc = 0.f;
+    pdl_wait();
+    pdl_trigger();
     for (long long b = s0; b < s1; b += CV_THREADS) {
         const long long s = b + threadIdx.x;
         const bool hit = s < s1 && a.idx[s] == id;
@@ -861,15 +871,12 @@ moe_status moe_balance_loss(const moe_layer_desc* d, const float* logits, const 
     p += al((size_t)a.blocks * (a.E + 1) * 4);
     a.part_z = reinterpret_cast<float*>(p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define CALL(L, EPL, V4) balance_loss_kernel<L, EPL, V4><<<a.blocks, threads, 0, st>>>(a)
+    moe_status r = MOE_OK;
+#define CALL(L, EPL, V4) r = launch_dependent(balance_loss_kernel<L, EPL, V4>, dim3(a.blocks), threads, 0, 1, st, a)
     MOE_LANES(a.E, CALL);
 #undef CALL
-    count_launch();
-    if (a.blocks > 1) {
-        balance_loss_finish_kernel<<<LOSS_CLUSTER, LOSS_THREADS, 0, st>>>(a);
-        count_launch();
-    }
-    return cuda_status(cudaGetLastError());
+    if (r != MOE_OK || a.blocks == 1) return r;
+    return launch_dependent(balance_loss_finish_kernel, dim3(LOSS_CLUSTER), LOSS_THREADS, 0, LOSS_CLUSTER, st, a);
 }
 
 moe_status moe_route_backward(const moe_layer_desc* d, const float* logits, const int32_t* topk_idx,
@@ -906,11 +913,11 @@ moe_status moe_route_backward(const moe_layer_desc* d, const float* logits, cons
     const long long per = (long long)RB_WARPS * G * (a.E > 128 ? rb_tokens<8>() : rb_tokens<1>());
     const int blocks = (int)std::min<long long>((a.T + per - 1) / per, 4ll * num_sms());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define CALL(L, EPL, V4) route_backward_kernel<L, EPL, V4><<<blocks, RB_THREADS, 0, st>>>(a)
+    moe_status r = MOE_OK;
+#define CALL(L, EPL, V4) r = launch_dependent(route_backward_kernel<L, EPL, V4>, dim3(blocks), RB_THREADS, 0, 1, st, a)
     MOE_LANES(a.E, CALL);
 #undef CALL
-    count_launch();
-    return cuda_status(cudaGetLastError());
+    return r;
 }
 
 moe_status moe_combine_backward(const moe_layer_desc* d, const moe_layer_weights* w, const void* dy,
@@ -973,28 +980,16 @@ moe_status moe_combine_backward(const moe_layer_desc* d, const moe_layer_weights
     const bool f32 = d->dtype == MOE_F32, dyf = f32 || d->out_f32;
     if (dgate || dy_sorted || dx || dconst_mix) {
         const int blocks = (int)std::min<long long>(((long long)a.T + CB_TOKENS - 1) / CB_TOKENS, 64ll * num_sms());
-        if (f32) combine_backward_kernel<float, float><<<blocks, CB_THREADS, 0, st>>>(a);
-        else if (dyf) combine_backward_kernel<__nv_bfloat16, float><<<blocks, CB_THREADS, 0, st>>>(a);
-        else combine_backward_kernel<__nv_bfloat16, __nv_bfloat16><<<blocks, CB_THREADS, 0, st>>>(a);
-        count_launch();
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        const moe_status r =
+            f32 ? launch_dependent(combine_backward_kernel<float, float>, dim3(blocks), CB_THREADS, 0, 1, st, a)
+            : dyf ? launch_dependent(combine_backward_kernel<__nv_bfloat16, float>, dim3(blocks), CB_THREADS, 0, 1, st, a)
+                  : launch_dependent(combine_backward_kernel<__nv_bfloat16, __nv_bfloat16>, dim3(blocks), CB_THREADS, 0, 1, st, a);
+        if (r != MOE_OK) return r;
     }
-    if (dconst_vec) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(CV_CLUSTER * cdiv(a.d, CV_THREADS), a.n_const);
-        cfg.blockDim = dim3(CV_THREADS);
-        cfg.stream = st;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim = {CV_CLUSTER, 1, 1};
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        const cudaError_t e = dyf ? cudaLaunchKernelEx(&cfg, const_vec_grad_kernel<float>, a)
-                                  : cudaLaunchKernelEx(&cfg, const_vec_grad_kernel<__nv_bfloat16>, a);
-        count_launch();
-        if (e != cudaSuccess) return MOE_ERR_CUDA;
-    }
-    return cuda_status(cudaGetLastError());
+    if (!dconst_vec) return MOE_OK;
+    const dim3 grid(CV_CLUSTER * cdiv(a.d, CV_THREADS), a.n_const);
+    return dyf ? launch_dependent(const_vec_grad_kernel<float>, grid, CV_THREADS, 0, CV_CLUSTER, st, a)
+               : launch_dependent(const_vec_grad_kernel<__nv_bfloat16>, grid, CV_THREADS, 0, CV_CLUSTER, st, a);
 }
 
 }  // extern "C"
