@@ -305,7 +305,8 @@ def _rp(t):
         return None
     if not t.is_cuda:
         raise ValueError("libmoe takes CUDA tensors")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    st = t.stride()
+    if len(st) != 2 or (st[1] != 1 and t.shape[1] > 1):
         raise ValueError("libmoe takes 2-D tensors with contiguous rows")
     return t.data_ptr()
 

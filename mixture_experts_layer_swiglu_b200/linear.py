@@ -30,7 +30,7 @@ class Linear:
     """A dense product with device-resident weights w [N, K] and bias [N] (fp32, or None).
 
     forward(x [M, K]) and backward(x, dy [M, N]) take any M; the descriptor gives the other sizes, the types
-    and the row stride of w.  The row strides of the other tensors are read from the tensors.  Nothing is kept
+    and the row stride of w.  The row strides of the other tensors are read from the tensors.  No tensor is kept
     from one call to the next: workspace and outputs come from torch's allocator on the call's stream.
     """
 
@@ -40,92 +40,97 @@ class Linear:
         self.out_dtype = torch.float32 if desc.out_f32 else self.dtype
         self.grad_dtype = torch.float32 if desc.grad_f32 else self.dtype
         self.w, self.bias = w, bias                  # keeps the tensors alive
-        self._check("w", w, desc.N, desc.K, self.dtype)
-        if w.stride(0) != (desc.ld_w or desc.K) and desc.N > 1:
+        self._device = w.get_device()                # -1: not on a GPU
+        self._last = None
+        if self._ld("w", w, desc.N, desc.K, self.dtype) not in (0, desc.ld_w or desc.K):
             raise ValueError(f"w: expected a row stride of {desc.ld_w or desc.K}, got {w.stride(0)}")
-        if bias is not None and (tuple(bias.shape) != (desc.N,) or bias.dtype != torch.float32):
-            raise ValueError(f"bias: expected a [{desc.N}] torch.float32 tensor, got {list(bias.shape)} {bias.dtype}")
+        if bias is not None and (bias.shape != (desc.N,) or bias.dtype is not torch.float32 or
+                                 bias.get_device() != self._device):
+            raise ValueError(f"bias: expected a [{desc.N}] torch.float32 tensor on {w.device}, got {list(bias.shape)} "
+                             f"{bias.dtype} on {bias.device}")
 
-    def _check(self, name, t, rows, cols, dtype) -> None:
+    def _ld(self, name, t, rows, cols, dtype) -> int:
+        """The row stride of a tensor that has to be [rows, cols] on the weights' device (0: none, or one row)."""
         if t is None:
-            return
-        if t.shape != (rows, cols) or t.dtype != dtype:
+            return 0
+        if t.dtype is not dtype or t.shape != (rows, cols):
             raise ValueError(f"{name}: expected a [{rows}, {cols}] {dtype} tensor, got {list(t.shape)} {t.dtype}")
         s0, s1 = t.stride()
         if cols > 1 and s1 != 1 or rows > 1 and s0 < cols:
             raise ValueError(f"{name}: expected contiguous rows that do not overlap, got strides {(s0, s1)}")
-        if t.device != self.w.device:
-            raise ValueError(f"{name}: on {t.device}, the weights are on {self.w.device}")
+        if t.get_device() != self._device:
+            raise ValueError(f"{name}: expected on {self.w.device}, got {t.device}")
+        return s0 if rows > 1 else 0
 
-    def _call_desc(self, x, y=None, residual=None, z=None, dx=None) -> abi.MoELinearDesc:
+    def _sized(self, M, ld_x, ld_y, ld_r, ld_z, ld_dx):
+        """(descriptor of a call, its workspace bytes forward and backward); the last call's, if the sizes are the same."""
+        key = (M, ld_x, ld_y, ld_r, ld_z, ld_dx)
+        last = self._last
+        if last is not None and last[0] == key:
+            return last
         d = self.desc
-        M = x.shape[0]
-
-        def ld(t):          # (one row has no stride)
-            return t.stride(0) if t is not None and M > 1 else 0
-
-        return abi.MoELinearDesc(M, d.N, d.K, d.dtype, d.act, d.out_f32, d.grad_f32, ld(x), d.ld_w, ld(y), ld(residual),
-                                 ld(z), ld(dx))
+        cd = abi.MoELinearDesc(M, d.N, d.K, d.dtype, d.act, d.out_f32, d.grad_f32, ld_x, d.ld_w, ld_y, ld_r, ld_z, ld_dx)
+        self._last = (key, cd, abi.moe_linear_workspace_size(cd), abi.moe_linear_backward_workspace_size(cd))
+        return self._last
 
     def _on(self, stream):
         """(context, stream) of a call: where it allocates and launches.  The weights' device need not be current."""
-        if not self.w.is_cuda:
+        if self._device < 0:
             raise ValueError("libmoe takes CUDA tensors")
         if stream is None:
-            if self.w.get_device() == torch.cuda.current_device():
+            if self._device == torch.cuda.current_device():
                 return _HERE, None
             return torch.cuda.device(self.w.device), None
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=self.w.device)
         if stream.device != self.w.device:
-            raise ValueError(f"stream: on {stream.device}, the weights are on {self.w.device}")
+            raise ValueError(f"stream: expected on {self.w.device}, got {stream.device}")
         return torch.cuda.stream(stream), stream
 
     def forward(self, x: torch.Tensor, residual=None, y=None, z=None, stream=None) -> torch.Tensor:
         """y = act(x w^T + bias) + residual; the pre-activation is written to z where one is given."""
-        d = self.desc
+        N, K = self.desc.N, self.desc.K
         M = x.shape[0] if x.dim() == 2 else -1
-        self._check("x", x, M, d.K, self.dtype)
-        self._check("residual", residual, M, d.N, self.out_dtype)
-        self._check("y", y, M, d.N, self.out_dtype)
-        self._check("z", z, M, d.N, self.dtype)
+        ld_x = self._ld("x", x, M, K, self.dtype)
+        ld_r = self._ld("residual", residual, M, N, self.out_dtype)
+        ld_y = self._ld("y", y, M, N, self.out_dtype)
+        ld_z = self._ld("z", z, M, N, self.dtype)
         ctx, stream = self._on(stream)
         with ctx:
             if y is None:
-                y = torch.empty((M, d.N), dtype=self.out_dtype, device=x.device)
-            cd = self._call_desc(x, y, residual, z)
-            need = abi.moe_linear_workspace_size(cd)
-            ws = torch.empty((need,), dtype=torch.uint8, device=x.device) if need > 0 else None
+                y = x.new_empty((M, N), dtype=self.out_dtype)
+            _, cd, need, _ = self._sized(M, ld_x, ld_y, ld_r, ld_z, 0)
+            ws = x.new_empty((need,), dtype=torch.uint8) if need > 0 else None
             abi.moe_linear(cd, x, self.w, self.bias, residual, y, z, ws, stream)
         return y
 
     def backward(self, x: torch.Tensor, dy: torch.Tensor, z=None, dx=None, dw=None, db=None, need_dx: bool = True,
                  need_dw: bool = True, need_db: bool | None = None, stream=None):
         """(dx, dw, db); one that is not needed is None (db by default: only with a bias).  z: as forward wrote it."""
-        d = self.desc
+        N, K = self.desc.N, self.desc.K
         M = x.shape[0] if x.dim() == 2 else -1
-        self._check("x", x, M, d.K, self.dtype)
-        self._check("dy", dy, M, d.N, self.out_dtype)
-        self._check("z", z, M, d.N, self.dtype)
-        self._check("dx", dx, M, d.K, self.dtype)
-        self._check("dw", dw, d.N, d.K, self.grad_dtype)
-        if z is None and d.act != abi.MOE_ACT_NONE:
+        ld_x = self._ld("x", x, M, K, self.dtype)
+        ld_dy = self._ld("dy", dy, M, N, self.out_dtype)
+        ld_z = self._ld("z", z, M, N, self.dtype)
+        ld_dx = self._ld("dx", dx, M, K, self.dtype)
+        if self._ld("dw", dw, N, K, self.grad_dtype) not in (0, K):
+            raise ValueError("dw: expected contiguous rows without gaps")
+        if z is None and self.desc.act != abi.MOE_ACT_NONE:
             raise ValueError("z: the gradient of an activation needs the pre-activation")
-        if db is not None and (tuple(db.shape) != (d.N,) or db.dtype != torch.float32):
-            raise ValueError(f"db: expected a [{d.N}] torch.float32 tensor, got {list(db.shape)} {db.dtype}")
+        if db is not None and (db.shape != (N,) or db.dtype is not torch.float32 or db.get_device() != self._device):
+            raise ValueError(f"db: expected a [{N}] torch.float32 tensor on {self.w.device}, got {list(db.shape)} {db.dtype}")
         ctx, stream = self._on(stream)
         with ctx:
             if dx is None and need_dx:
-                dx = torch.empty((M, d.K), dtype=self.dtype, device=x.device)
+                dx = x.new_empty((M, K))
             if dw is None and need_dw:
-                dw = torch.empty((d.N, d.K), dtype=self.grad_dtype, device=x.device)
+                dw = x.new_empty((N, K), dtype=self.grad_dtype)
             if db is None and (self.bias is not None if need_db is None else need_db):
-                db = torch.empty((d.N,), dtype=torch.float32, device=x.device)
+                db = x.new_empty((N,), dtype=torch.float32)
             if dx is None and dw is None and db is None:
                 return None, None, None
-            cd = self._call_desc(x, dy, None, z, dx)
-            need = abi.moe_linear_backward_workspace_size(cd)
-            ws = torch.empty((need,), dtype=torch.uint8, device=x.device) if need > 0 else None
+            _, cd, _, need = self._sized(M, ld_x, ld_dy, 0, ld_z, ld_dx)
+            ws = x.new_empty((need,), dtype=torch.uint8) if need > 0 else None
             abi.moe_linear_backward(cd, x, self.w, z, dy, dx, dw, db, ws, stream)
         return dx, dw, db
 
