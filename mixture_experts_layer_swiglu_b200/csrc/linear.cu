@@ -289,15 +289,29 @@ moe_status launch_dz(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
 }
 
 // ------------------------------------------------------------ packed rows
-// [rows, cols] bf16 to rows of ld_dst elements (a TMA tensor's row stride is a
-// multiple of 16 bytes).  What lies between cols and ld_dst is never read.
-__global__ void __launch_bounds__(256) linear_pack_kernel(const __nv_bfloat16* src, long long ld_src, int rows, int cols,
-                                                          __nv_bfloat16* dst, long long ld_dst)
+// bf16 rows to rows of a multiple of 8 elements (a TMA tensor's row stride is a
+// multiple of 16 bytes); both operands of a call in one launch.  What lies
+// between a row's end and its stride is never read.
+struct PackJob {
+    const __nv_bfloat16* src;
+    __nv_bfloat16* dst;
+    long long ld_src, ld_dst;
+    int rows, cols;
+};
+
+__global__ void __launch_bounds__(256) linear_pack_kernel(const PackJob p, const PackJob q)
 {
     pdl_wait();
     pdl_trigger();
-    for (long long r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int c = threadIdx.x; c < cols; c += 256) dst[r * ld_dst + c] = src[r * ld_src + c];
+    for (long long i = blockIdx.x; i < (long long)p.rows + q.rows; i += gridDim.x) {
+        const bool first = i < p.rows;
+        const long long r = first ? i : i - p.rows;
+        const __nv_bfloat16* src = (first ? p.src + r * p.ld_src : q.src + r * q.ld_src);
+        __nv_bfloat16* dst = (first ? p.dst + r * p.ld_dst : q.dst + r * q.ld_dst);
+        const int cols = first ? p.cols : q.cols;
+#pragma unroll 8
+        for (int c = threadIdx.x; c < cols; c += 256) dst[c] = src[c];
+    }
 }
 
 inline long long up8(long long n) { return (n + 7) & ~7ll; }
@@ -311,15 +325,21 @@ size_t packed_bytes(bool f32, long long rows, long long cols, long long ld)
 {
     return f32 || ld % 8 == 0 ? 0 : al((size_t)rows * up8(cols) * 2);
 }
-moe_status packed(const void* p, int rows, int cols, long long ld, char*& ws, cudaStream_t st, Rows& r)
+PackJob pack_job(Rows& r, int rows, int cols, char*& ws)
 {
-    r = Rows{p, ld};
-    if (ld % 8 == 0) return MOE_OK;
-    r = Rows{ws, up8(cols)};
+    if (!r.p || r.ld % 8 == 0) return PackJob{};
+    const PackJob j{static_cast<const __nv_bfloat16*>(r.p), reinterpret_cast<__nv_bfloat16*>(ws), r.ld, up8(cols), rows, cols};
+    r = Rows{ws, j.ld_dst};
     ws += al((size_t)rows * r.ld * 2);
-    return launch_dependent(linear_pack_kernel, dim3(std::min(rows, 8 * num_sms())), 256, 0, 1, st,
-                            static_cast<const __nv_bfloat16*>(p), ld, rows, cols,
-                            static_cast<__nv_bfloat16*>(const_cast<void*>(r.p)), r.ld);
+    return j;
+}
+// Packs x and w where they need it (a null one is not used by the call).
+moe_status pack(Rows& x, Rows& w, const Lin& l, char* ws, cudaStream_t st)
+{
+    const PackJob p = pack_job(x, l.M, l.K, ws), q = pack_job(w, l.N, l.K, ws);
+    const long long rows = (long long)p.rows + q.rows;
+    if (rows == 0) return MOE_OK;
+    return launch_dependent(linear_pack_kernel, dim3((unsigned)std::min<long long>(rows, 8 * num_sms())), 256, 0, 1, st, p, q);
 }
 
 // dz needs no buffer of its own where it is dy as it stands.
@@ -388,9 +408,9 @@ moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* w, co
     const LinEpilogue epi{bias, residual, z, y, l.ld_y, l.ld_r, l.ld_z, l.act, l.of32, l.f32};
     if (!l.f32) {
         char* ws = static_cast<char*>(workspace);
-        Rows xr, wr;
-        moe_status e = packed(x, l.M, l.K, l.ld_x, ws, st, xr);
-        if (e != MOE_OK || (e = packed(w, l.N, l.K, l.ld_w, ws, st, wr)) != MOE_OK) return e;
+        Rows xr{x, l.ld_x}, wr{w, l.ld_w};
+        const moe_status e = pack(xr, wr, l, ws, st);
+        if (e != MOE_OK) return e;
         return launch_linear_tc(TcProduct{wr.p, xr.p, wr.ld, xr.ld, 0, 0, 1, 0, l.M, l.N, l.K, epi}, st);
     }
     return launch_linear_simt(SimtProduct{static_cast<const float*>(x), static_cast<const float*>(w), l.ld_x, 1, l.ld_w, 1, l.M, l.N, l.K, epi}, st);
@@ -448,13 +468,13 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
             return s;
     }
     const Rows g{b.dz ? dz : dy, b.dz ? ld_dz : l.ld_y};
+    Rows xr{dw ? x : nullptr, l.ld_x}, wr{dx ? w : nullptr, l.ld_w};
+    if (!l.f32 && (s = pack(xr, wr, l, ws, st)) != MOE_OK) return s;
     if (dx) {
         const LinEpilogue epi{nullptr, nullptr, nullptr, dx, l.ld_dx, 0, 0, MOE_ACT_NONE, l.f32, 0};
         if (l.f32) {
             s = launch_linear_simt(SimtProduct{static_cast<const float*>(g.p), static_cast<const float*>(w), g.ld, 1, 1, l.ld_w, l.M, l.K, l.N, epi}, st);
         } else {
-            Rows wr;
-            if ((s = packed(w, l.N, l.K, l.ld_w, ws, st, wr)) != MOE_OK) return s;
             s = launch_linear_tc(TcProduct{wr.p, g.p, wr.ld, g.ld, 1, 0, 1, 0, l.M, l.K, l.N, epi}, st);
         }
         if (s != MOE_OK) return s;
@@ -464,8 +484,6 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         if (l.f32) {
             s = launch_linear_simt(SimtProduct{static_cast<const float*>(g.p), static_cast<const float*>(x), 1, g.ld, 1, l.ld_x, l.N, l.K, l.M, epi}, st);
         } else {
-            Rows xr;
-            if ((s = packed(x, l.M, l.K, l.ld_x, ws, st, xr)) != MOE_OK) return s;
             s = launch_linear_tc(TcProduct{xr.p, g.p, xr.ld, g.ld, 1, 1, parts, dz_step(l), l.N, l.K, l.M, epi}, st);
         }
         if (s != MOE_OK) return s;

@@ -553,16 +553,19 @@ __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8])
 }
 
 constexpr int CB_SPLIT = 4;                  // warps per token
-constexpr int CB_TOKENS = 2;                 // tokens per block
+constexpr int CB_TOKENS = 1;                 // tokens per block (two: 2-7% slower)
 constexpr int CB_THREADS = CB_SPLIT * CB_TOKENS * 32;
 constexpr int CB_C = 2;                      // 8-element chunks per lane and step
 constexpr int CB_MAXK = 32;
 
 // A token's row is split over 4 warps; each lane holds its chunks of dy in
 // registers and goes over the slots: one read of the expert's row for the dot
-// product, one write of the gated row.
+// product, one write of the gated row.  Bound by memory: the next slot's row is
+// loaded while one is at work, with six blocks per SM (8192 x 2048, top-6 and
+// two shared experts: 190 -> 126 us, 5.6 TB/s).  Loading the next token's slots
+// ahead too cost registers and measured 139 us.
 template <typename T, typename TO>
-__global__ void __launch_bounds__(CB_THREADS) combine_backward_kernel(const CombineBwdArgs a)
+__global__ void __launch_bounds__(CB_THREADS, 6) combine_backward_kernel(const CombineBwdArgs a)
 {
     __shared__ int s_e[CB_TOKENS][CB_MAXK], s_r[CB_TOKENS][CB_MAXK];
     __shared__ float s_g[CB_TOKENS][CB_MAXK], s_a1[CB_TOKENS][CB_MAXK], s_a2[CB_TOKENS][CB_MAXK];
@@ -589,12 +592,11 @@ __global__ void __launch_bounds__(CB_THREADS) combine_backward_kernel(const Comb
             if (live && lane < a.k) {
                 e = a.idx[t * a.k + lane];
                 g = a.gate[t * a.k + lane];
-                bool bad = e < 0 || e >= n_ids;
-                if (!bad && e < a.n_ffn) {
-                    r = a.row_of[t * a.k + lane];
-                    bad = r < 0 || r >= a.rows_cap;
+                r = a.row_of ? a.row_of[t * a.k + lane] : -1;
+                if (e < 0 || e >= n_ids || (e < a.n_ffn && (r < 0 || r >= a.rows_cap))) {
+                    set_status(MOE_ERR_DEVICE_BOUNDS);
+                    e = -1;
                 }
-                if (bad) { set_status(MOE_ERR_DEVICE_BOUNDS); e = -1; }
                 if (e >= copy0 && e < const0) coef = g;
                 if (e >= const0 && a.cmix) {
                     a1 = a.cmix[(t * a.n_const + (e - const0)) * 2 + 0];
@@ -637,41 +639,53 @@ __global__ void __launch_bounds__(CB_THREADS) combine_backward_kernel(const Comb
                     s = group_sum<32>(s);
                     if (lane == 0) s_dot[tib][a.k][part] += s;
                 }
-                for (int j = 0; j < a.k; ++j) {
-                    const int e = s_e[tib][j];
-                    const float g = s_g[tib][j];
-                    float s = 0.f;
-                    if (e >= 0 && e < a.n_ffn) {
-                        const long long r = s_r[tib][j];
+                // the next slot's expert row is on its way while this one's is at work
+                float u[2][CB_C][8];
+                auto fetch = [&](int j, float (&q)[CB_C][8]) {
+                    if (j >= a.k || !a.dgate || s_e[tib][j] < 0 || s_e[tib][j] >= a.n_ffn) return;
+                    const float* row = a.ys + (long long)s_r[tib][j] * a.d;
 #pragma unroll
-                        for (int c = 0; c < CB_C; ++c) {
-                            const int i = ib + lane + 32 * c;
-                            if (i >= i1) continue;
-                            if (a.dgate) {
-                                float u[8];
-                                ld8(a.ys + r * a.d + i * 8, u);
-                                s += dot8(u, v[c]);
+                    for (int c = 0; c < CB_C; ++c)
+                        if (ib + lane + 32 * c < i1) ld8(row + (ib + lane + 32 * c) * 8, q[c]);
+                };
+                fetch(0, u[0]);
+                for (int j0 = 0; j0 < a.k; j0 += 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = j0 + h;
+                        if (j >= a.k) break;
+                        fetch(j + 1, u[h ^ 1]);
+                        const int e = s_e[tib][j];
+                        const float g = s_g[tib][j];
+                        float s = 0.f;
+                        if (e >= 0 && e < a.n_ffn) {
+                            const long long r = s_r[tib][j];
+#pragma unroll
+                            for (int c = 0; c < CB_C; ++c) {
+                                const int i = ib + lane + 32 * c;
+                                if (i >= i1) continue;
+                                if (a.dgate) s += dot8(u[h][c], v[c]);
+                                if (dys) {
+                                    float q[8];
+#pragma unroll
+                                    for (int x8 = 0; x8 < 8; ++x8) q[x8] = g * v[c][x8];
+                                    st8(dys + r * a.d + i * 8, q);
+                                }
                             }
-                            if (dys) {
-                                float u[8];
+                            if (!a.dgate) continue;
+                        } else if (e >= const0 && want_dot) {
 #pragma unroll
-                                for (int q = 0; q < 8; ++q) u[q] = g * v[c][q];
-                                st8(dys + r * a.d + i * 8, u);
+                            for (int c = 0; c < CB_C; ++c) {
+                                const int i = ib + lane + 32 * c;
+                                float q[8];
+                                if (i < i1) { ld8(cvec + (long long)(e - const0) * a.d + i * 8, q); s += dot8(q, v[c]); }
                             }
+                        } else {
+                            continue;
                         }
-                        if (!a.dgate) continue;
-                    } else if (e >= const0 && want_dot) {
-#pragma unroll
-                        for (int c = 0; c < CB_C; ++c) {
-                            const int i = ib + lane + 32 * c;
-                            float u[8];
-                            if (i < i1) { ld8(cvec + (long long)(e - const0) * a.d + i * 8, u); s += dot8(u, v[c]); }
-                        }
-                    } else {
-                        continue;
+                        s = group_sum<32>(s);
+                        if (lane == 0) s_dot[tib][j][part] += s;
                     }
-                    s = group_sum<32>(s);
-                    if (lane == 0) s_dot[tib][j][part] += s;
                 }
                 if (dys)
                     for (int sh = 0; sh < a.n_shared; ++sh) {
@@ -731,58 +745,101 @@ __global__ void __launch_bounds__(CB_THREADS) combine_backward_kernel(const Comb
 
 // dconst_vec[c] = sum over the slots of constant expert c of g a2 dy_t.  A
 // cluster of 8 blocks shares one (256 columns, c): each block lists the
-// matching slots of its token range in order and sums their rows, then the
-// blocks' sums are added in order.
+// matching slots of its token range in order, 1024 at a time, and sums their
+// rows (four columns per thread, four rows side by side); the blocks' sums are
+// added in order.
 constexpr int CV_CLUSTER = 8;
 constexpr int CV_THREADS = 256;
+constexpr int CV_COLS = 256;
+constexpr int CV_SLOTS = 4 * CV_THREADS;
 
 template <typename TO>
 __global__ void __launch_bounds__(CV_THREADS) const_vec_grad_kernel(const CombineBwdArgs a)
 {
-    __shared__ float s_acc[CV_THREADS];
-    __shared__ float s_w[CV_THREADS];
-    __shared__ int s_t[CV_THREADS];
-    __shared__ int s_n[CV_THREADS / 32 + 1];
+    __shared__ float s_acc[4][CV_COLS];
+    __shared__ float s_sum[CV_COLS];
+    __shared__ float s_w[CV_SLOTS];
+    __shared__ int s_t[CV_SLOTS];
+    __shared__ int s_n[CV_THREADS / 32];
     const int rank = blockIdx.x % CV_CLUSTER, slice = blockIdx.x / CV_CLUSTER, c = blockIdx.y;
     const int id = a.n_ffn + a.n_zero + a.n_copy + c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = slice * CV_THREADS + threadIdx.x;
+    const int side = threadIdx.x / 64, cl4 = threadIdx.x % 64 * 4;          // row side by side, first of four columns
+    const int col = slice * CV_COLS + cl4;                                  // (d is a multiple of 8)
     const long long S = (long long)a.T * a.k;
     const long long s0 = S * rank / CV_CLUSTER, s1 = S * (rank + 1) / CV_CLUSTER;
     const TO* dy = reinterpret_cast<const TO*>(a.dy);
-    float acc = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     pdl_wait();
     pdl_trigger();
-    for (long long b = s0; b < s1; b += CV_THREADS) {
-        const long long s = b + threadIdx.x;
-        const bool hit = s < s1 && a.idx[s] == id;
-        const unsigned m = __ballot_sync(FULL, hit);
-        if (lane == 0) s_n[warp] = __popc(m);
+    for (long long b = s0; b < s1; b += CV_SLOTS) {
+        // thread i looks at slots 4 i .. 4 i + 3 of the chunk
+        bool hit[4];
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const long long s = b + threadIdx.x * 4 + q;
+            hit[q] = s < s1 && a.idx[s] == id;
+            n += hit[q];
+        }
+        int before = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) s_n[warp] = before;
+        before -= n;
         __syncthreads();
-        int before = 0, total = 0;
+        int total = 0;
+#pragma unroll
         for (int w = 0; w < CV_THREADS / 32; ++w) {
             before += w < warp ? s_n[w] : 0;
             total += s_n[w];
         }
-        if (hit) {
-            const int at = before + __popc(m & ((1u << lane) - 1u));
-            const int t = (int)(s / a.k);
-            s_t[at] = t;
-            s_w[at] = a.gate[s] * a.cmix[((long long)t * a.n_const + c) * 2 + 1];
-        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (hit[q]) {
+                const long long s = b + threadIdx.x * 4 + q;
+                const long long t = s / a.k;
+                s_t[before] = (int)t;
+                s_w[before] = a.gate[s] * a.cmix[(t * a.n_const + c) * 2 + 1];
+                ++before;
+            }
         __syncthreads();
         if (col < a.d)
-#pragma unroll 8
-            for (int i = 0; i < total; ++i) acc = fmaf(s_w[i], (float)dy[(long long)s_t[i] * a.d + col], acc);
+#pragma unroll 4
+            for (int i = side; i < total; i += 4) {
+                const TO* p = dy + (long long)s_t[i] * a.d + col;
+                const float w = s_w[i];
+                if constexpr (sizeof(TO) == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(p);
+                    acc[0] = fmaf(w, bf16_lo(x.x), acc[0]);
+                    acc[1] = fmaf(w, bf16_hi(x.x), acc[1]);
+                    acc[2] = fmaf(w, bf16_lo(x.y), acc[2]);
+                    acc[3] = fmaf(w, bf16_hi(x.y), acc[3]);
+                } else {
+                    const float4 x = *reinterpret_cast<const float4*>(p);
+                    acc[0] = fmaf(w, x.x, acc[0]);
+                    acc[1] = fmaf(w, x.y, acc[1]);
+                    acc[2] = fmaf(w, x.z, acc[2]);
+                    acc[3] = fmaf(w, x.w, acc[3]);
+                }
+            }
         __syncthreads();
     }
-    s_acc[threadIdx.x] = acc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_acc[side][cl4 + i] = acc[i];
+    __syncthreads();
+    s_sum[threadIdx.x] = (s_acc[0][threadIdx.x] + s_acc[1][threadIdx.x]) + (s_acc[2][threadIdx.x] + s_acc[3][threadIdx.x]);
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
-    if (rank == 0 && col < a.d) {
+    const int mine = slice * CV_COLS + threadIdx.x;
+    if (rank == 0 && mine < a.d) {
         float v = 0.f;
-        for (int q = 0; q < CV_CLUSTER; ++q) v += cl.map_shared_rank(s_acc, q)[threadIdx.x];
-        a.dcvec[(long long)c * a.d + col] = v;
+#pragma unroll
+        for (int q = 0; q < CV_CLUSTER; ++q) v += cl.map_shared_rank(s_sum, q)[threadIdx.x];
+        a.dcvec[(long long)c * a.d + mine] = v;
     }
     cl.sync();
 }
@@ -987,7 +1044,7 @@ moe_status moe_combine_backward(const moe_layer_desc* d, const moe_layer_weights
         if (r != MOE_OK) return r;
     }
     if (!dconst_vec) return MOE_OK;
-    const dim3 grid(CV_CLUSTER * cdiv(a.d, CV_THREADS), a.n_const);
+    const dim3 grid(CV_CLUSTER * cdiv(a.d, CV_COLS), a.n_const);
     return dyf ? launch_dependent(const_vec_grad_kernel<float>, grid, CV_THREADS, 0, CV_CLUSTER, st, a)
                : launch_dependent(const_vec_grad_kernel<__nv_bfloat16>, grid, CV_THREADS, 0, CV_CLUSTER, st, a);
 }
