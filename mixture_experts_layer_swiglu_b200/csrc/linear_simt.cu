@@ -1,5 +1,15 @@
 // linear_simt.cu -- the dense product on FMA pipes: fp32 layers (the tensor
 // cores' tf32 keeps 11 significant bits, fp32 results here keep all of them).
+//
+// A block computes a TILE x TILE piece of the output from 16-deep slices of both
+// operands in shared memory (two buffers; the next slice is on its way to
+// registers while one is multiplied).  A thread holds (TILE / 16)^2 outputs and
+// multiplies them with packed fp32x2 FMAs.  128 x 128: 64 outputs, four 16-byte
+// shared loads per 64 FMAs: 48 TFLOP/s where the tiles fill the GPU (4736 x
+// 1024 x 2048), 0.65 of the FMA pipes' peak; 128 x 256 with one block per SM
+// measured 46.  64 x 64: for outputs too small to fill the GPU with the former; a cluster of up to 8 blocks then also
+// splits the contraction and adds its tiles through distributed shared memory,
+// in order of rank.
 
 #include <cooperative_groups.h>
 
@@ -16,80 +26,124 @@ namespace {
 constexpr int LS_THREADS = 256;
 constexpr int LS_BK = 16;
 
-// A TILE x 16 piece of an operand into registers: threads run along the
-// dimension that is contiguous in memory.
+// One operand's side of the tile: element (i, k) at i * rs + k * ks, one of them 1.
+struct Side {
+    const float* p;
+    long long rs, ks;
+    int n;                   // extent of i
+    int vec;                 // 16-byte loads along the contiguous index are aligned
+};
+
+// A TILE x 16 slice into registers, in pieces of four along the contiguous
+// index; a piece that is cut by an edge (or not aligned) is loaded element by element.
 template <int TILE>
-__device__ __forceinline__ void fetch(const float* base, long long rs, long long ks, int r0, int rows, int k0, int k1,
-                                      float (&v)[TILE / 16])
+__device__ __forceinline__ void fetch(const Side& s, int i0, int k0, int K, float4 (&v)[TILE / 64])
 {
     const int t = threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < TILE / 16; ++i) {
-        const int r = ks == 1 ? t / LS_BK + (LS_THREADS / LS_BK) * i : t % TILE;
-        const int k = ks == 1 ? t % LS_BK : t / TILE + (LS_THREADS / TILE) * i;
-        v[i] = (r0 + r < rows && k0 + k < k1) ? base[(long long)(r0 + r) * rs + (long long)(k0 + k) * ks] : 0.f;
+    for (int q = 0; q < TILE / 64; ++q) {
+        const int piece = t + q * LS_THREADS;
+        const bool kc = s.ks == 1;
+        const int i = i0 + (kc ? piece / 4 : piece % (TILE / 4) * 4), k = k0 + (kc ? piece % 4 * 4 : piece / (TILE / 4));
+        const float* p = s.p + (long long)i * s.rs + (long long)k * s.ks;
+        const int left = kc ? (i < s.n ? K - k : 0) : (k < K ? s.n - i : 0);
+        if (s.vec && left >= 4) {
+            v[q] = *reinterpret_cast<const float4*>(p);
+        } else {
+            v[q].x = left > 0 ? p[0] : 0.f;
+            v[q].y = left > 1 ? p[1] : 0.f;
+            v[q].z = left > 2 ? p[2] : 0.f;
+            v[q].w = left > 3 ? p[3] : 0.f;
+        }
     }
 }
 
 template <int TILE>
-__device__ __forceinline__ void stash(float (*s)[TILE + 4], long long ks, const float (&v)[TILE / 16])
+__device__ __forceinline__ void stash(float (*d)[TILE + 4], const Side& s, const float4 (&v)[TILE / 64])
 {
     const int t = threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < TILE / 16; ++i) {
-        const int r = ks == 1 ? t / LS_BK + (LS_THREADS / LS_BK) * i : t % TILE;
-        const int k = ks == 1 ? t % LS_BK : t / TILE + (LS_THREADS / TILE) * i;
-        s[k][r] = v[i];
+    for (int q = 0; q < TILE / 64; ++q) {
+        const int piece = t + q * LS_THREADS;
+        if (s.ks == 1) {
+            const int i = piece / 4, k = piece % 4 * 4;
+            d[k][i] = v[q].x;
+            d[k + 1][i] = v[q].y;
+            d[k + 2][i] = v[q].z;
+            d[k + 3][i] = v[q].w;
+        } else {
+            *reinterpret_cast<float4*>(&d[piece / (TILE / 4)][piece % (TILE / 4) * 4]) = v[q];
+        }
     }
 }
 
-// One TILE x TILE output tile per cluster; the cluster's blocks split K and add
-// their partial tiles in order of rank through distributed shared memory.
+// Packed pairs of fp32: {v, v}, and d += x * y on both halves.
+__device__ __forceinline__ uint64_t twice(float v)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void fma_pair(uint64_t& d, uint64_t x, uint64_t y)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(x), "l"(y));
+}
+__device__ __forceinline__ float half_of(uint64_t v, int i)
+{
+    return __uint_as_float((uint32_t)(i ? v >> 32 : v));
+}
+
 template <int TILE>
-__global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProduct p, int splits, int tiles_c)
+__global__ void __launch_bounds__(LS_THREADS, TILE == 128 ? 2 : 4)
+linear_simt_kernel(const Side P, const Side Q, int K, const LinEpilogue epi, int splits, int tiles_c)
 {
     constexpr int F = TILE / 16;                 // outputs per thread and direction
-    extern __shared__ float s_dyn[];
+    extern __shared__ __align__(16) float s_dyn[];
     float(*sp)[LS_BK][TILE + 4] = reinterpret_cast<float(*)[LS_BK][TILE + 4]>(s_dyn);
     float(*sq)[LS_BK][TILE + 4] = sp + 2;
     const int rank = blockIdx.x % splits, tile = blockIdx.x / splits;
     const int r0 = (tile / tiles_c) * TILE, c0 = (tile % tiles_c) * TILE;
-    const int blocks_k = cdiv(p.K, LS_BK);
+    const int blocks_k = cdiv(K, LS_BK);
     const int kb0 = (int)((long long)blocks_k * rank / splits), kb1 = (int)((long long)blocks_k * (rank + 1) / splits);
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[F][F];
+    uint64_t acc2[F][F / 2];                     // columns 2 j and 2 j + 1
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < F / 2; ++j) acc2[i][j] = 0;
     pdl_wait();
     pdl_trigger();
-    float vp[F], vq[F];
+    float4 vp[TILE / 64], vq[TILE / 64];
     if (kb0 < kb1) {
-        fetch<TILE>(p.P, p.p_rs, p.p_ks, r0, p.R, kb0 * LS_BK, p.K, vp);
-        fetch<TILE>(p.Q, p.q_rs, p.q_ks, c0, p.C, kb0 * LS_BK, p.K, vq);
+        fetch<TILE>(P, r0, kb0 * LS_BK, K, vp);
+        fetch<TILE>(Q, c0, kb0 * LS_BK, K, vq);
     }
     int buf = 0;
     for (int kb = kb0; kb < kb1; ++kb, buf ^= 1) {
-        stash<TILE>(sp[buf], p.p_ks, vp);
-        stash<TILE>(sq[buf], p.q_ks, vq);
+        stash<TILE>(sp[buf], P, vp);
+        stash<TILE>(sq[buf], Q, vq);
         __syncthreads();
         if (kb + 1 < kb1) {
-            fetch<TILE>(p.P, p.p_rs, p.p_ks, r0, p.R, (kb + 1) * LS_BK, p.K, vp);
-            fetch<TILE>(p.Q, p.q_rs, p.q_ks, c0, p.C, (kb + 1) * LS_BK, p.K, vq);
+            fetch<TILE>(P, r0, (kb + 1) * LS_BK, K, vp);
+            fetch<TILE>(Q, c0, (kb + 1) * LS_BK, K, vq);
         }
 #pragma unroll
         for (int k = 0; k < LS_BK; ++k) {
-            float a[F], b[F];
+            float a[F];
+            uint64_t b[F / 2];
 #pragma unroll
             for (int i = 0; i < F; i += 4) {
                 *reinterpret_cast<float4*>(a + i) = *reinterpret_cast<const float4*>(&sp[buf][k][ty * 4 + 16 * i]);
-                *reinterpret_cast<float4*>(b + i) = *reinterpret_cast<const float4*>(&sq[buf][k][tx * 4 + 16 * i]);
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sq[buf][k][tx * 4 + 16 * i]);
+                b[i / 2] = x.x;
+                b[i / 2 + 1] = x.y;
             }
 #pragma unroll
-            for (int i = 0; i < F; ++i)
+            for (int i = 0; i < F; ++i) {
+                const uint64_t aa = twice(a[i]);
 #pragma unroll
-                for (int j = 0; j < F; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < F / 2; ++j) fma_pair(acc2[i][j], aa, b[j]);
+            }
         }
     }
     // row / column of accumulator i: ty * 4 + (i % 4) + 64 * (i / 4)
@@ -99,7 +153,7 @@ __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProdu
 #pragma unroll
             for (int j = 0; j < F; ++j) {
                 const int r = r0 + ty * 4 + (i % 4) + 64 * (i / 4), c = c0 + tx * 4 + (j % 4) + 64 * (j / 4);
-                if (r < p.R && c < p.C) lin_store(p.epi, r, c, acc[i][j]);
+                if (r < P.n && c < Q.n) lin_store(epi, r, c, half_of(acc2[i][j / 2], j & 1));
             }
         return;
     }
@@ -108,17 +162,19 @@ __global__ void __launch_bounds__(LS_THREADS) linear_simt_kernel(const SimtProdu
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j)
-            red[(ty * 4 + (i % 4) + 64 * (i / 4)) * TILE + tx * 4 + (j % 4) + 64 * (j / 4)] = acc[i][j];
+        for (int j = 0; j < F; j += 4)
+            *reinterpret_cast<ulonglong2*>(&red[(ty * 4 + (i % 4) + 64 * (i / 4)) * TILE + tx * 4 + 64 * (j / 4)]) =
+                make_ulonglong2(acc2[i][j / 2], acc2[i][j / 2 + 1]);
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
     const int per = TILE / splits;
     for (int i = threadIdx.x; i < per * TILE; i += LS_THREADS) {
         const int r = rank * per + i / TILE, c = i % TILE;
-        if (r0 + r >= p.R || c0 + c >= p.C) continue;
+        if (r0 + r >= P.n || c0 + c >= Q.n) continue;
         float v = 0.f;
+#pragma unroll 8
         for (int q = 0; q < splits; ++q) v += cl.map_shared_rank(red, q)[r * TILE + c];
-        lin_store(p.epi, r0 + r, c0 + c, v);
+        lin_store(epi, r0 + r, c0 + c, v);
     }
     cl.sync();
 }
@@ -132,20 +188,36 @@ moe_status launch(const SimtProduct& p, int splits, cudaStream_t st)
     const int smem = std::max(4 * LS_BK * (TILE + 4) * 4, splits > 1 ? TILE * TILE * 4 : 0);
     auto* fn = linear_simt_kernel<TILE>;
     if (ensure_smem_attr(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return MOE_ERR_CUDA;
-    return launch_dependent(fn, dim3((unsigned)(tiles * splits)), LS_THREADS, smem, splits, st, p, splits, tiles_c);
+    auto side = [](const float* b, long long rs, long long ks, int n) {
+        return Side{b, rs, ks, n, (rs == 1 ? ks : rs) % 4 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0};
+    };
+    return launch_dependent(fn, dim3((unsigned)(tiles * splits)), LS_THREADS, smem, splits, st,
+                            side(p.P, p.p_rs, p.p_ks, p.R), side(p.Q, p.q_rs, p.q_ks, p.C), p.K, p.epi, splits, tiles_c);
 }
 
 }  // namespace
 
+// The tile and split of the smallest estimate, in us: a 16-deep step of a
+// 128 x 128 tile takes 1.3 alone on an SM and 2.5 beside another block, one of a
+// 64 x 64 tile 0.5 alone and 0.36 for each of up to four; 1.5 to add the tiles of a split.
 moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st)
 {
-    const long long big = (long long)cdiv(p.R, 128) * cdiv(p.C, 128);
-    const int sms = num_sms();
-    if (big >= 2 * sms) return launch<128>(p, 1, st);
-    const long long tiles = (long long)cdiv(p.R, 64) * cdiv(p.C, 64);
-    int splits = 1;
-    while (splits < 8 && tiles * splits < sms && p.K >= 64 * splits) splits *= 2;
-    return launch<64>(p, splits, st);
+    const int nkb = cdiv(p.K, LS_BK), sms = num_sms();
+    int tile = 64, splits = 1;
+    double least = 1e30;
+    for (int t : {64, 128}) {
+        const long long tiles = (long long)cdiv(p.R, t) * cdiv(p.C, t);
+        for (int S = 1; S <= 8; S *= 2) {
+            if (S > 1 && (t == 128 || nkb < 2 * S)) continue;
+            const long long blocks = tiles * S, room = (t == 128 ? 2 : 4) * (long long)sms;
+            const long long waves = (blocks + room - 1) / room;
+            const long long beside = std::min<long long>((blocks + sms - 1) / sms, t == 128 ? 2 : 4);
+            const double step = t == 128 ? (beside == 1 ? 1.3 : 2.5) : std::max(0.5, 0.36 * beside);
+            const double us = waves * (cdiv(nkb, S) * step + 1.0) + (S > 1 ? 1.5 : 0.0);
+            if (us < least) { least = us; tile = t; splits = S; }
+        }
+    }
+    return tile == 128 ? launch<128>(p, splits, st) : launch<64>(p, splits, st);
 }
 
 }  // namespace moe
