@@ -29,6 +29,13 @@
 
 #include "linear.h"
 
+// fp32 results: the tensor cores add each 16 steps of the contraction to the
+// accumulator with a rounding toward zero, so an error of about 1e-8 of the sum
+// per 16 steps piles up (K = 2048: 1.4e-6, five times an fp32 FMA chain's).  A
+// product that is not rounded to bf16 afterwards therefore changes accumulators
+// every 512 steps (PROMOTE), and the epilogue's warps add them up in registers
+// under the MMAs of the next.
+
 namespace moe {
 
 namespace {
@@ -37,10 +44,12 @@ constexpr int KB = 64;                          // contraction elements per stag
 constexpr int CB = 128;                         // output columns of one CTA's tile (TMEM lanes)
 constexpr int A_BYTES = CB * KB * 2;            // 16 KB
 constexpr int BOX_BYTES = 64 * 128;             // an MN-major box: 64 steps of k x 64 elements
+constexpr int PROMOTE_STEPS = 512 / KB;         // steps of KB in one accumulator of an fp32 result
 
 struct TcArgs {
     int R, C, nkb, bn;
     int tiles_r, tiles_c, group_r;
+    int chunk;                                  // steps of the contraction that stay in one accumulator
     int stages, splits, per_log;                // split form; log2 of the rows that each CTA of a cluster finishes
     uint32_t a_bytes, b_bytes;                  // bytes of one stage and CTA (split form; pair: a_bytes is A_BYTES)
     int part, boxes, acc_part;                  // three-part B: column distance of the parts, boxes per stage, accumulator distance
@@ -259,6 +268,42 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
     }
 }
 
+// Accumulator columns j .. j + 31 of this lane.  The parts of a three-part B
+// enter one MMA side by side, as three 64-wide boxes (N = 192) or, while the
+// three together have at most 64 columns, as one (as three MMAs they took 75
+// clocks apiece, whatever their N): their accumulators are added here, the
+// small ones first.
+template <int PARTS>
+__device__ __forceinline__ void acc_load(uint32_t t, int j, int part, uint32_t (&v)[32])
+{
+    tmem_ld32(PARTS == 3 ? t + 2 * part + j : t + j, v);
+    tc_wait_ld_regs(v);
+    if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int p = 1; p >= 0; --p) {
+            uint32_t m[32];
+            tmem_ld32(t + p * part + j, m);
+            tc_wait_ld_regs(m);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(m[i]));
+        }
+    }
+}
+
+// sum += the accumulator columns j .. j + 31 (first: sum = them).
+template <int PARTS>
+__device__ __forceinline__ void acc_add(uint32_t t, int j, int part, bool first, uint32_t (&sum)[32])
+{
+    if (first) {
+        acc_load<PARTS>(t, j, part, sum);
+        return;
+    }
+    uint32_t v[32];
+    acc_load<PARTS>(t, j, part, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
+}
+
 // ------------------------------------------------------------ pair form
 constexpr int PR_MAX_STAGES = 10;
 constexpr int PR_EPI_WARPS = 8;                                // two per TMEM lane quarter, alternate 32-row chunks
@@ -283,7 +328,7 @@ __device__ __forceinline__ void tile_at(const TcArgs& a, int tile, int& tr, int&
     tr = band * a.group_r + in - tc * h;
 }
 
-template <bool AMN, bool BMN, int ACT>
+template <bool AMN, bool BMN, int ACT, bool PROMOTE>
 __global__ void __launch_bounds__(PR_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
@@ -374,23 +419,30 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             uint32_t ph = 0, aph = 0;
             bool bad = false;
             for (int tile = cluster; tile < total && !bad; tile += n_clusters) {
-                if (!warp_wait(&acc_empty[acc], aph ^ 1)) { *abort_flag = 1; break; }
-                tc_fence_after();
-                const uint32_t d = tmem_base + acc * 256;
+                int left = 0;                                  // steps that this accumulator still takes
+                uint32_t d = 0;
                 for (int kb = 0; kb < a.nkb; ++kb) {
+                    const bool begin = left == 0;
+                    if (begin) {
+                        if (!warp_wait(&acc_empty[acc], aph ^ 1)) { *abort_flag = 1; bad = true; break; }
+                        tc_fence_after();
+                        d = tmem_base + acc * 256;
+                        left = min(PROMOTE ? a.chunk : a.nkb, a.nkb - kb);
+                    }
                     if (!warp_wait(&full[s], ph)) { *abort_flag = 1; bad = true; break; }
                     const uint64_t ad = ad0 + (uint64_t)(s * (A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * b16);
+                    --left;
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < KB / 16; ++kk)
-                            tc_mma_bf16_pair(d, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, (kb | kk) != 0);
+                            tc_mma_bf16_pair(d, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, !begin || kk != 0);
                         tc_commit_pair(&empty[s], 0x3);
-                        if (kb + 1 == a.nkb) tc_commit_pair(&acc_full[acc], 0x3);
+                        if (left == 0) tc_commit_pair(&acc_full[acc], 0x3);
                     }
                     __syncwarp();
                     if (++s == a.stages) { s = 0; ph ^= 1; }
+                    if (left == 0 && ++acc == 2) { acc = 0; aph ^= 1; }
                 }
-                if (++acc == 2) { acc = 0; aph ^= 1; }
             }
             // every MMA issued has completed before the CTAs may leave
             if (elect_one()) tc_commit_pair(mma_done, 0x1);
@@ -410,20 +462,42 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             const int rows = (int)min((long long)a.bn, a.R - r0);
             const float bias = a.epi.bias && c0 + lane < a.C ? a.epi.bias[c0 + lane] : 0.f;
             uint4 res[8] = {};
-            if (a.staged & ST_RES) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, lane);
-            if (!warp_wait(&acc_full[acc], aph)) { *abort_flag = 1; break; }
-            tc_fence_after();
-            const uint32_t t = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
-            for (int j = half * 32; j < rows; j += 64) {
-                uint32_t v[32];
-                tmem_ld32(t + j, v);
-                tc_wait_ld_regs(v);
-                if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 64, c0, bias, st);
+            if (!PROMOTE && (a.staged & ST_RES)) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, lane);
+            const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16);
+            if constexpr (PROMOTE) {
+                uint32_t sum0[32], sum1[32];                   // of this warp's two chunks of rows (bn <= 128)
+                const bool two = half * 32 + 64 < rows;
+                bool bad = false;
+                for (int kb = 0; kb < a.nkb && !bad; kb += a.chunk) {
+                    if (!warp_wait(&acc_full[acc], aph)) { *abort_flag = 1; bad = true; break; }
+                    tc_fence_after();
+                    acc_add<1>(t0 + acc * 256, half * 32, 0, kb == 0, sum0);
+                    if (two) acc_add<1>(t0 + acc * 256, half * 32 + 64, 0, kb == 0, sum1);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8 * acc);
+                    if (++acc == 2) { acc = 0; aph ^= 1; }
+                }
+                if (bad) break;
+                if (a.staged & ST_RES) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, lane);
+                if (half * 32 < rows && c0 < a.C)
+                    epilogue32<ACT>(a, &tmOut, &tmZ, sum0, res, r0 + half * 32, rows - half * 32, 64, c0, bias, st);
+                if (two && c0 < a.C)
+                    epilogue32<ACT>(a, &tmOut, &tmZ, sum1, res, r0 + half * 32 + 64, rows - half * 32 - 64, 64, c0, bias, st);
+            } else {
+                if (!warp_wait(&acc_full[acc], aph)) { *abort_flag = 1; break; }
+                tc_fence_after();
+                for (int j = half * 32; j < rows; j += 64) {
+                    uint32_t v[32];
+                    tmem_ld32(t0 + acc * 256 + j, v);
+                    tc_wait_ld_regs(v);
+                    if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 64, c0, bias, st);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8 * acc);
+                if (++acc == 2) { acc = 0; aph ^= 1; }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8 * acc);
-            if (++acc == 2) { acc = 0; aph ^= 1; }
         }
         if (lane == 0) bulk_wait_read<0>();        // the buffers are read; the writes end with the kernel
     }
@@ -441,30 +515,6 @@ constexpr int SP_THREADS = 192;               // (eight epilogue warps: slower b
 constexpr int SP_MAX_STAGES = 12;
 
 __host__ __device__ constexpr int sp_tmem_cols(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
-
-// Accumulator columns j .. j + 31 of this lane.  The parts of a three-part B
-// enter one MMA side by side, as three 64-wide boxes (N = 192) or, while the
-// three together have at most 64 columns, as one (as three MMAs they took 75
-// clocks apiece, whatever their N): their accumulators are added here, the
-// small ones first.
-template <int PARTS>
-__device__ __forceinline__ void acc_load(uint32_t t, int j, int part, uint32_t (&v)[32])
-{
-    tmem_ld32(t + j, v);
-    if constexpr (PARTS == 3) {
-        uint32_t m[32], l[32];
-        tmem_ld32(t + part + j, m);
-        tmem_ld32(t + 2 * part + j, l);
-        tc_wait_ld_regs(l);
-        tc_wait_ld_regs(m);
-        tc_wait_ld_regs(v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] = __float_as_uint(__uint_as_float(v[i]) + (__uint_as_float(m[i]) + __uint_as_float(l[i])));
-    } else {
-        tc_wait_ld_regs(v);
-    }
-}
 
 // Four neighbouring elements of a row, as one access where strides and length allow (vec).
 __device__ __forceinline__ void row4_load(const LinEpilogue& e, int vec, long long r, int c, int C, float (&v)[4])
@@ -503,7 +553,7 @@ __device__ __forceinline__ void row4_store(void* base, long long ld, int f32, in
 
 // Shared memory: stages x (A, then the parts of B), the partial sums that the
 // cluster's CTAs send here ([splits][bn / splits][128] fp32), the barriers.
-template <bool AMN, bool BMN, int ACT, int PARTS>
+template <bool AMN, bool BMN, int ACT, int PARTS, bool PROMOTE>
 __global__ void __launch_bounds__(SP_THREADS, 2)
 linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
@@ -517,8 +567,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
                                           (stage_bytes < A_BYTES ? A_BYTES - stage_bytes : 0));
     uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + (a.splits > 1 ? a.bn * CB * 4 : 0));
     uint64_t* empty = full + SP_MAX_STAGES;
-    uint64_t* acc_full = empty + SP_MAX_STAGES;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    uint64_t* acc_full = empty + SP_MAX_STAGES;                 // two of each
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -528,7 +579,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     const long long r0 = (long long)tr * a.bn;
     const int kb0 = (int)((long long)a.nkb * rank / a.splits), kb1 = (int)((long long)a.nkb * (rank + 1) / a.splits);
     static_assert(PARTS == 1 || (PARTS == 3 && BMN), "three parts: 64-wide boxes");
-    const int cols = PARTS == 3 ? 256 : sp_tmem_cols(a.bn);
+    const int cols = PARTS == 3 ? (a.boxes == 1 ? 64 : 256) : sp_tmem_cols(a.bn);      // one accumulator; PROMOTE: two
 
     // The producer starts its loads before the block's first barrier; the
     // cluster's barrier is only announced here, and awaited before the first
@@ -536,14 +587,14 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     bool waited = a.splits == 1;
     if (a.splits > 1) cluster_arrive_relaxed();
     if (warp == 0) {
-        // (full, empty and acc_full lie in a row: a barrier per lane)
-        if (lane < 2 * SP_MAX_STAGES + 1) mbar_init(full + lane, 1);
+        // (full, empty, acc_full and acc_empty lie in a row: a barrier per lane)
+        if (lane < 2 * SP_MAX_STAGES + 4) mbar_init(full + lane, lane < 2 * SP_MAX_STAGES + 2 ? 1 : 4);
         if (lane == 31) *abort_flag = 0;
         fence_barrier_init();
         __syncwarp();
         pdl_wait();
     } else {
-        if (warp == 1) { tmem_alloc(tmem_slot, cols); tmem_relinquish(); }
+        if (warp == 1) { tmem_alloc(tmem_slot, PROMOTE ? 2 * cols : cols); tmem_relinquish(); }
         tc_fence_before();
         block_sync<SP_THREADS>();
         tc_fence_after();
@@ -589,40 +640,76 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         const uint32_t idesc = idesc_bf16_f32(CB, PARTS == 3 ? 64 * a.boxes : a.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
         const uint64_t ad0 = operand_desc<AMN>(smem), bd0 = operand_desc<BMN>(smem + a.a_bytes);
         const uint32_t stage16 = stage_bytes >> 4;
-        int s = 0;
-        uint32_t ph = 0;
+        int s = 0, left = 0, acc = 0;
+        uint32_t ph = 0, aph = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
+            const bool begin = left == 0;
+            if (begin) {
+                if (PROMOTE) {
+                    if (!warp_wait(&acc_empty[acc], aph ^ 1)) { *abort_flag = 1; break; }
+                    tc_fence_after();
+                }
+                left = min(PROMOTE ? a.chunk : kb1 - kb0, kb1 - kb);
+            }
             if (!warp_wait(&full[s], ph)) { *abort_flag = 1; break; }
             const uint64_t ad = ad0 + (uint64_t)(s * stage16), bd = bd0 + (uint64_t)(s * stage16);
+            --left;
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < KB / 16; ++kk)
-                    tc_mma_bf16(tmem_base, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, kb > kb0 || kk > 0);
+                    tc_mma_bf16(tmem_base + acc * cols, ad + kk * kStepDesc<AMN>, bd + kk * kStepDesc<BMN>, idesc, !begin || kk > 0);
                 tc_commit(&empty[s]);
+                if (left == 0) tc_commit(&acc_full[acc]);
             }
             __syncwarp();
             if (++s == a.stages) { s = 0; ph ^= 1; }
+            if (PROMOTE && left == 0 && ++acc == 2) { acc = 0; aph ^= 1; }
         }
-        if (elect_one()) tc_commit(acc_full);
-        __syncwarp();
     } else {
         const int q = warp & 3, cl = q * 32 + lane, cq = c0 + q * 32;
         const uint32_t t = *tmem_slot + ((uint32_t)(q * 32) << 16);
         uint4 res[8] = {};
         const int rows = (int)min((long long)a.bn, a.R - r0);
-        if (a.splits == 1 && (a.staged & ST_RES)) residual_load(a, res, r0, rows, cq, lane);
-        const bool ok = warp_wait(acc_full, 0) && !*abort_flag;
-        tc_fence_after();
+        const bool want_res = a.splits == 1 && (a.staged & ST_RES);
+        if (!PROMOTE && want_res) residual_load(a, res, r0, rows, cq, lane);
+        // PROMOTE: the accumulators' sums, at most 64 rows of the tile
+        uint32_t sum0[32], sum1[32];
+        bool ok = true;
+        if constexpr (PROMOTE) {
+            int acc = 0;
+            uint32_t aph = 0;
+            for (int kb = kb0; kb < kb1 && ok; kb += a.chunk) {
+                if (want_res && kb + a.chunk >= kb1) residual_load(a, res, r0, rows, cq, lane);
+                ok = warp_wait(&acc_full[acc], aph);
+                if (!ok) break;
+                tc_fence_after();
+                acc_add<PARTS>(t + acc * cols, 0, a.acc_part, kb == kb0, sum0);
+                if (a.bn > 32) acc_add<PARTS>(t + acc * cols, 32, a.acc_part, kb == kb0, sum1);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[acc]);
+                if (++acc == 2) { acc = 0; aph ^= 1; }
+            }
+        } else {
+            ok = warp_wait(acc_full, 0);
+            tc_fence_after();
+        }
+        ok = ok && !*abort_flag;
         if (!ok) {
             *abort_flag = 1;
         } else if (a.splits == 1) {
             // the stages are no longer needed: every copy has landed and every MMA has read it
             Staging st{smem + (warp - 2) * 2 * STAGE_ROWS, 0, lane};
             const float bias = a.epi.bias && c0 + cl < a.C ? a.epi.bias[c0 + cl] : 0.f;
-            for (int j = 0; j < rows; j += 32) {
-                uint32_t v[32];
-                acc_load<PARTS>(t, j, a.acc_part, v);          // (bn = 16: the upper half is not used, the allocation has 32 columns)
-                if (cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 32, cq, bias, st);
+            if constexpr (PROMOTE) {
+                if (cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, sum0, res, r0, rows, 32, cq, bias, st);
+                if (rows > 32 && cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, sum1, res, r0 + 32, rows - 32, 32, cq, bias, st);
+            } else {
+                for (int j = 0; j < rows; j += 32) {
+                    uint32_t v[32];
+                    acc_load<PARTS>(t, j, a.acc_part, v);      // (bn = 16: the upper half is not used, the allocation has 32 columns)
+                    if (cq < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 32, cq, bias, st);
+                }
             }
             if (lane == 0) bulk_wait_read<0>();
         } else {
@@ -630,15 +717,23 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             cluster_wait();
             waited = true;
             const uint32_t mine = smem_u32(red) + (uint32_t)((((rank << a.per_log) * CB) + cl) * 4);
-            for (int j0 = 0; j0 < a.bn; j0 += 32) {
-                uint32_t v[32];
-                acc_load<PARTS>(t, j0, a.acc_part, v);
+            auto send = [&](const uint32_t (&v)[32], int j0) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int j = j0 + i;
                     if (j < a.bn)
                         st_cluster_f32(mapa_shared(mine + (uint32_t)((j & ((1 << a.per_log) - 1)) * CB * 4), j >> a.per_log),
                                        __uint_as_float(v[i]));
+                }
+            };
+            if constexpr (PROMOTE) {
+                send(sum0, 0);
+                if (a.bn > 32) send(sum1, 32);
+            } else {
+                for (int j0 = 0; j0 < a.bn; j0 += 32) {
+                    uint32_t v[32];
+                    acc_load<PARTS>(t, j0, a.acc_part, v);
+                    send(v, j0);
                 }
             }
         }
@@ -648,7 +743,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(*tmem_slot, cols);
+        tmem_dealloc(*tmem_slot, PROMOTE ? 2 * cols : cols);
     }
     if (a.splits == 1) return;
     // A warp finishes a row of 128 columns at a time, four per lane.  (32 columns
@@ -777,6 +872,10 @@ int sp_stages(const TcProduct& p, int bn, int splits, int occ)
     return std::max(0, std::min(SP_MAX_STAGES, room / sp_stage_bytes(p, bn)));
 }
 
+// Whether a CTA that takes 1 / splits of the contraction is to change accumulators
+// on the way (the product's fp32 sums are the result).
+bool promoted(const TcProduct& p, int splits) { return p.epi.out_f32 && cdiv(cdiv(p.K, KB), splits) > PROMOTE_STEPS; }
+
 // Which form and tile: the smallest estimate of the time in us.  Its terms are
 // fits to measurements on a B200 (errors of 10-15%):
 //   pair   a step (64 of the contraction) 0.13 + 0.00057 bn, the rest of a launch
@@ -784,7 +883,8 @@ int sp_stages(const TcProduct& p, int bn, int splits, int occ)
 //   split  a step 0.18 + 0.0004 bn with one CTA on an SM, 0.15 + 0.0024 bn with
 //          two, and at least a loaded memory latency over the stages in flight;
 //          at least the loads of all tiles at 13 TB/s, the most that L2 gave;
-//          the rest 4.6 + 0.0065 bn, and 1 + 0.02 bn to add partial tiles.
+//          the rest 4.6 + 0.0065 bn, and 1 + 0.02 bn to add partial tiles;
+//   fp32 results that change accumulators: 0.07 a step (pair), 0.35 a change (split).
 Plan choose(const TcProduct& p)
 {
     const int nkb = cdiv(p.K, KB), sms = num_sms();
@@ -792,10 +892,11 @@ Plan choose(const TcProduct& p)
     double least = 1e30;
     if (p.b_parts == 1) {
         const int tc = cdiv(p.C, 2 * CB);
-        for (int bn = 32; bn <= 256; bn += 32) {
+        for (int bn = 32; bn <= (promoted(p, 1) ? 128 : 256); bn += 32) {
             const long long tiles = (long long)tc * cdiv(p.R, bn);
             const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
-            const double t = waves * (nkb * (0.13 + 0.00057 * bn) + 0.3) + 4.1 + 0.0105 * bn;
+            const double step = 0.13 + 0.00057 * bn + (promoted(p, 1) ? 0.07 : 0.0);
+            const double t = waves * (nkb * step + 0.3) + 4.1 + 0.0105 * bn;
             if (t < least) { least = t; best = Plan{1, bn, 1, 0, 1, 8}; }
         }
     }
@@ -804,7 +905,7 @@ Plan choose(const TcProduct& p)
         if (p.b_parts > 1 && bn != 64) continue;
         const long long tiles = (long long)tc * cdiv(p.R, bn);
         for (int S = 1; S <= 8; S *= 2) {
-            if (S > nkb) continue;
+            if (S > nkb || (bn > 64 && promoted(p, S))) continue;
             const int slots = S == 8 ? sms * 13 / 16 : S == 4 ? sms * 8 / 9 : sms;     // whole clusters within the GPCs
             const int occ = tiles * S > slots && sp_stages(p, bn, S, 2) >= 3 ? 2 : 1;
             const int stages = sp_stages(p, bn, S, occ);
@@ -813,7 +914,8 @@ Plan choose(const TcProduct& p)
             const int n = p.b_parts == 3 ? 64 * sp_boxes(p) : bn;
             const double step = std::max(occ == 2 ? 0.15 + 0.0024 * n : 0.18 + 0.0004 * n, 1.5 / stages);
             const double loads = (double)tiles * nkb * sp_stage_bytes(p, bn) / 13e6;
-            const double t = std::max(waves * (cdiv(nkb, S) * step + 0.5 + 0.0065 * bn), loads) + 4.1 +
+            const double sums = promoted(p, S) ? 0.35 * cdiv(cdiv(nkb, S), PROMOTE_STEPS) : 0.0;
+            const double t = std::max(waves * (cdiv(nkb, S) * step + sums + 0.5 + 0.0065 * bn), loads) + 4.1 +
                              (S > 1 ? 1.0 + 0.02 * bn : 0.0);
             if (t < least) { least = t; best = Plan{0, bn, S, stages, occ, 1}; }
         }
@@ -821,7 +923,7 @@ Plan choose(const TcProduct& p)
     return best;
 }
 
-template <bool AMN, bool BMN, int ACT>
+template <bool AMN, bool BMN, int ACT, bool PROMOTE>
 moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
 {
     CUtensorMap mA, mB, mO, mZ;
@@ -844,14 +946,15 @@ moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
         return MOE_ERR_CUDA;
     if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
     a.stages = pr_stages((int)a.b_bytes);
-    auto* fn = linear_pair_kernel<AMN, BMN, ACT>;
+    a.chunk = PROMOTE_STEPS;
+    auto* fn = linear_pair_kernel<AMN, BMN, ACT, PROMOTE>;
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), PR_SMEM);
     if (e != cudaSuccess) return cuda_status(e);
     const int clusters = (int)std::min<long long>(tiles, num_sms() / 2);
     return launch_dependent(fn, dim3(2 * clusters), PR_THREADS, PR_SMEM, 2, st, mA, mB, mO, mZ, a);
 }
 
-template <bool AMN, bool BMN, int ACT, int PARTS>
+template <bool AMN, bool BMN, int ACT, int PARTS, bool PROMOTE>
 moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
 {
     CUtensorMap mA, mB, mO, mZ;
@@ -880,33 +983,39 @@ moe_status launch_split(const TcProduct& p, const Plan& pl, cudaStream_t st)
     if (!(BMN ? operand_map(&mB, p.B, width, p.K, p.ldb, 64) : operand_map(&mB, p.B, p.K, p.R, p.ldb, pl.bn)))
         return MOE_ERR_CUDA;
     if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
-    auto* fn = linear_split_kernel<AMN, BMN, ACT, PARTS>;
+    a.chunk = PROMOTE_STEPS;
+    auto* fn = linear_split_kernel<AMN, BMN, ACT, PARTS, PROMOTE>;
     const int smem = pl.stages * sp_stage_bytes(p, pl.bn) + sp_other_bytes(p, pl.bn, pl.splits);
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem);
     if (e != cudaSuccess) return cuda_status(e);
     return launch_dependent(fn, dim3((unsigned)ctas), SP_THREADS, smem, pl.splits, st, mA, mB, mO, mZ, a);
 }
 
+template <bool AMN, bool BMN, int ACT, bool PROMOTE>
+moe_status launch_form(const TcProduct& p, const Plan& pl, cudaStream_t st)
+{
+    return pl.pair ? launch_pair<AMN, BMN, ACT, PROMOTE>(p, pl, st) : launch_split<AMN, BMN, ACT, 1, PROMOTE>(p, pl, st);
+}
+
 moe_status launch_plan(const TcProduct& p, const Plan& pl, cudaStream_t st)
 {
+    const bool pro = promoted(p, pl.pair ? 1 : pl.splits);
     if (!p.a_mn && !p.b_mn && p.b_parts == 1) {
         switch (p.epi.act) {
-            case MOE_ACT_NONE:
-                return pl.pair ? launch_pair<false, false, MOE_ACT_NONE>(p, pl, st) : launch_split<false, false, MOE_ACT_NONE, 1>(p, pl, st);
-            case MOE_ACT_RELU:
-                return pl.pair ? launch_pair<false, false, MOE_ACT_RELU>(p, pl, st) : launch_split<false, false, MOE_ACT_RELU, 1>(p, pl, st);
-            case MOE_ACT_SILU:
-                return pl.pair ? launch_pair<false, false, MOE_ACT_SILU>(p, pl, st) : launch_split<false, false, MOE_ACT_SILU, 1>(p, pl, st);
-            default:
-                return pl.pair ? launch_pair<false, false, MOE_ACT_GELU>(p, pl, st) : launch_split<false, false, MOE_ACT_GELU, 1>(p, pl, st);
+#define FORM(ACT) return pro ? launch_form<false, false, ACT, true>(p, pl, st) : launch_form<false, false, ACT, false>(p, pl, st)
+            case MOE_ACT_NONE: FORM(MOE_ACT_NONE);
+            case MOE_ACT_RELU: FORM(MOE_ACT_RELU);
+            case MOE_ACT_SILU: FORM(MOE_ACT_SILU);
+            default: FORM(MOE_ACT_GELU);
+#undef FORM
         }
     }
-    if (p.epi.act != MOE_ACT_NONE) return MOE_ERR_UNSUPPORTED;
-    if (p.a_mn && !p.b_mn && p.b_parts == 1)
-        return pl.pair ? launch_pair<true, false, MOE_ACT_NONE>(p, pl, st) : launch_split<true, false, MOE_ACT_NONE, 1>(p, pl, st);
-    if (p.a_mn && p.b_mn && p.b_parts == 1)
-        return pl.pair ? launch_pair<true, true, MOE_ACT_NONE>(p, pl, st) : launch_split<true, true, MOE_ACT_NONE, 1>(p, pl, st);
-    if (p.a_mn && p.b_mn && p.b_parts == 3 && !pl.pair) return launch_split<true, true, MOE_ACT_NONE, 3>(p, pl, st);
+    if (p.epi.act != MOE_ACT_NONE || !p.a_mn) return MOE_ERR_UNSUPPORTED;
+    if (!p.b_mn && p.b_parts == 1) return launch_form<true, false, MOE_ACT_NONE, false>(p, pl, st);
+    if (p.b_mn && p.b_parts == 1)
+        return pro ? launch_form<true, true, MOE_ACT_NONE, true>(p, pl, st) : launch_form<true, true, MOE_ACT_NONE, false>(p, pl, st);
+    if (p.b_mn && p.b_parts == 3 && !pl.pair)
+        return pro ? launch_split<true, true, MOE_ACT_NONE, 3, true>(p, pl, st) : launch_split<true, true, MOE_ACT_NONE, 3, false>(p, pl, st);
     return MOE_ERR_UNSUPPORTED;
 }
 
