@@ -2,9 +2,13 @@
 // workspace, the pass that forms dz and db, the copies of rows that TMA cannot
 // address, and the order of the products.
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "linear.h"
+
+namespace cg = cooperative_groups;
 
 namespace moe {
 
@@ -40,9 +44,10 @@ moe_status read_desc(const moe_linear_desc* d, Lin& l)
 
 // ------------------------------------------------------------ dz and db
 // dz = dy act'(z) (written unless dz is null) and the column sums of the
-// unrounded dz, in one pass bound by memory.  A block covers COLS columns of a
-// range of rows; the block's sums go to part [chunks, N], or straight to db when
-// there is one range.  Two layouts:
+// unrounded dz, in one pass bound by memory.  A block covers a slice of the
+// columns of a range of rows.  Up to 8 ranges form a cluster, whose sums are
+// added through distributed shared memory; more leave theirs in part [ranges, N]
+// for a second kernel.  Two layouts:
 //   vec   rows of 16-byte pieces: a lane holds 8 neighbouring columns, a warp 256
 //         columns of a row (8192 x 4096, db alone: 26 us with ReLU, 38 us with
 //         SiLU, whose slope then takes the time);
@@ -60,7 +65,28 @@ struct DzArgs {
     long long ld_dy, ld_z, ld_dz;
     int M, N, act, rows;         // rows per range
     int parts, step, lanes;      // lanes: columns of a warp in the plain layout (8, 16 or 32)
+    int ranges;                  // blocks side by side in the grid; a cluster if db
+    float* db;                   // non-null: written by the cluster (part is unused)
 };
+
+// The sums of a block's columns, in shared memory, to where they belong.
+__device__ __forceinline__ void dz_sums(const DzArgs& a, float* sum, int cols, int c0, int range)
+{
+    if (a.db) {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        if (range == 0)
+            for (int i = threadIdx.x; i < cols && c0 + i < a.N; i += DZ_THREADS) {
+                float v = 0.f;
+                for (int q = 0; q < a.ranges; ++q) v += cl.map_shared_rank(sum, q)[i];
+                a.db[c0 + i] = v;
+            }
+        cl.sync();
+    } else if (a.part) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < cols && c0 + i < a.N; i += DZ_THREADS) a.part[(long long)range * a.N + c0 + i] = sum[i];
+    }
+}
 
 // v as a sum of bf16 values: each part the nearest bf16 of what the parts
 // before it left (24 bits in three).  An infinity or NaN is its first part.
@@ -156,8 +182,8 @@ __global__ void __launch_bounds__(DZ_THREADS, 4) linear_dz_vec_kernel(const DzAr
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 256 + lane * 8;
-    const long long m0 = (long long)blockIdx.y * a.rows;
+    const int range = blockIdx.x % a.ranges, c0 = (int)(blockIdx.x / a.ranges) * 256, c = c0 + lane * 8;
+    const long long m0 = (long long)range * a.rows;
     const long long m1 = min((long long)a.M, m0 + a.rows);
     const TY* dy = static_cast<const TY*>(a.dy) + c;
     const TZ* z = static_cast<const TZ*>(a.z) + c;
@@ -183,15 +209,15 @@ __global__ void __launch_bounds__(DZ_THREADS, 4) linear_dz_vec_kernel(const DzAr
             dz_row<TZ, ACT>(a, y, zz, m * a.ld_dz + c, acc);
         }
     }
-    if (!a.part) return;
+    if (!a.part && !a.db) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[warp][lane * 8 + i] = acc[i];
     __syncthreads();
-    const int cc = blockIdx.x * 256 + threadIdx.x;
-    if (cc >= a.N) return;
     float v = 0.f;
     for (int w = 0; w < DZ_WARPS; ++w) v += s[w][threadIdx.x];
-    a.part[(long long)blockIdx.y * a.N + cc] = v;
+    __syncthreads();
+    s[0][threadIdx.x] = v;
+    dz_sums(a, s[0], 256, c0, range);
 }
 
 template <typename TY, typename TZ, int ACT>
@@ -201,8 +227,8 @@ __global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
     pdl_wait();
     pdl_trigger();
     const int sub = threadIdx.x / a.lanes, subs = DZ_THREADS / a.lanes;      // rows side by side in the block
-    const int c = blockIdx.x * a.lanes + threadIdx.x % a.lanes;
-    const long long m0 = (long long)blockIdx.y * a.rows;
+    const int range = blockIdx.x % a.ranges, c0 = (int)(blockIdx.x / a.ranges) * a.lanes, c = c0 + threadIdx.x % a.lanes;
+    const long long m0 = (long long)range * a.rows;
     const long long m1 = min((long long)a.M, m0 + a.rows);
     float acc = 0.f;
     if (c < a.N) {
@@ -226,13 +252,15 @@ __global__ void __launch_bounds__(DZ_THREADS) linear_dz_kernel(const DzArgs a)
             }
         }
     }
-    if (!a.part) return;
+    if (!a.part && !a.db) return;
     s[threadIdx.x] = acc;
     __syncthreads();
-    if (threadIdx.x >= a.lanes || c >= a.N) return;
     float v = 0.f;
-    for (int i = 0; i < subs; ++i) v += s[i * a.lanes + threadIdx.x];
-    a.part[(long long)blockIdx.y * a.N + c] = v;
+    if (threadIdx.x < a.lanes)
+        for (int i = 0; i < subs; ++i) v += s[i * a.lanes + threadIdx.x];
+    __syncthreads();
+    if (threadIdx.x < a.lanes) s[threadIdx.x] = v;
+    dz_sums(a, s, a.lanes, c0, range);
 }
 
 // The ranges' sums: 32 columns per block, the warps take the ranges in turn.
@@ -255,8 +283,9 @@ __global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, int 
     db[c] = v;
 }
 
-// Columns of a block, and the ranges of rows: about four blocks per SM, at
-// least 32 rows each, at most 256 ranges (their sums are added by one block).
+// Columns of a block, and the ranges of rows: at least 32 rows each, up to 256
+// rows a cluster of at most 8 of them, then about four blocks per SM and at most
+// 256 ranges (whose sums one block adds).
 bool dz_vec(const Lin& l, long long ld_dz)
 {
     return l.N % 8 == 0 && l.N >= 128 && l.ld_y % 8 == 0 && ld_dz % 8 == 0 && (l.act == MOE_ACT_NONE || l.ld_z % 8 == 0);
@@ -265,26 +294,29 @@ int dz_lanes(const Lin& l) { return l.N <= 8 ? 8 : l.N <= 16 ? 16 : 32; }
 int dz_chunks(const Lin& l, bool vec, int* rows)
 {
     const int slices = cdiv(l.N, vec ? 256 : dz_lanes(l));
-    const int chunks = std::max(1, std::min(std::min(cdiv(l.M, 32), 256), cdiv(4 * 148, slices)));
+    const int most = l.M <= 256 ? 8 : 256;
+    const int chunks = std::max(1, std::min(std::min(cdiv(l.M, 32), most), cdiv(4 * 148, slices)));
     *rows = cdiv(std::max(l.M, 1), chunks);
     return cdiv(std::max(l.M, 1), *rows);
 }
 
 template <typename TY, typename TZ, int ACT>
-moe_status launch_dz_t(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
+moe_status launch_dz_t(const DzArgs& a, bool vec, cudaStream_t st)
 {
-    return vec ? launch_dependent(linear_dz_vec_kernel<TY, TZ, ACT>, dim3(cdiv(a.N, 256), chunks), DZ_THREADS, 0, 1, st, a)
-               : launch_dependent(linear_dz_kernel<TY, TZ, ACT>, dim3(cdiv(a.N, a.lanes), chunks), DZ_THREADS, 0, 1, st, a);
+    const int cluster = a.db ? a.ranges : 1;
+    const dim3 grid((unsigned)(cdiv(a.N, vec ? 256 : a.lanes) * a.ranges));
+    return vec ? launch_dependent(linear_dz_vec_kernel<TY, TZ, ACT>, grid, DZ_THREADS, 0, cluster, st, a)
+               : launch_dependent(linear_dz_kernel<TY, TZ, ACT>, grid, DZ_THREADS, 0, cluster, st, a);
 }
 
 template <typename TY, typename TZ>
-moe_status launch_dz(const DzArgs& a, bool vec, int chunks, cudaStream_t st)
+moe_status launch_dz(const DzArgs& a, bool vec, cudaStream_t st)
 {
     switch (a.act) {
-        case MOE_ACT_RELU: return launch_dz_t<TY, TZ, MOE_ACT_RELU>(a, vec, chunks, st);
-        case MOE_ACT_SILU: return launch_dz_t<TY, TZ, MOE_ACT_SILU>(a, vec, chunks, st);
-        case MOE_ACT_GELU: return launch_dz_t<TY, TZ, MOE_ACT_GELU>(a, vec, chunks, st);
-        default: return launch_dz_t<TY, TZ, MOE_ACT_NONE>(a, vec, chunks, st);
+        case MOE_ACT_RELU: return launch_dz_t<TY, TZ, MOE_ACT_RELU>(a, vec, st);
+        case MOE_ACT_SILU: return launch_dz_t<TY, TZ, MOE_ACT_SILU>(a, vec, st);
+        case MOE_ACT_GELU: return launch_dz_t<TY, TZ, MOE_ACT_GELU>(a, vec, st);
+        default: return launch_dz_t<TY, TZ, MOE_ACT_NONE>(a, vec, st);
     }
 }
 
@@ -458,12 +490,14 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* x, const vo
         a.lanes = dz_lanes(l);
         const bool vec = dz_vec(l, ld_dz);
         const int chunks = dz_chunks(l, vec, &a.rows);
-        a.part = db ? (chunks == 1 ? db : part) : nullptr;
-        s = l.f32 ? launch_dz<float, float>(a, vec, chunks, st)
-                  : l.of32 ? launch_dz<float, __nv_bfloat16>(a, vec, chunks, st)
-                           : launch_dz<__nv_bfloat16, __nv_bfloat16>(a, vec, chunks, st);
+        a.ranges = chunks;
+        a.db = chunks <= 8 ? db : nullptr;
+        a.part = db && !a.db ? part : nullptr;
+        s = l.f32 ? launch_dz<float, float>(a, vec, st)
+                  : l.of32 ? launch_dz<float, __nv_bfloat16>(a, vec, st)
+                           : launch_dz<__nv_bfloat16, __nv_bfloat16>(a, vec, st);
         if (s != MOE_OK) return s;
-        if (db && chunks > 1 &&
+        if (a.part &&
             (s = launch_dependent(linear_db_kernel, dim3(cdiv(l.N, 32)), 1024, 0, 1, st, part, chunks, l.N, db)) != MOE_OK)
             return s;
     }

@@ -858,7 +858,7 @@ void loss_blocks(int T, int E, int& blocks, int& per, int& threads)
     threads = 128;
     while (threads < LOSS_THREADS && 2 * threads < lanes) threads *= 2;
     const long long want = lanes <= 4 * LOSS_THREADS ? 1 : (lanes + 4 * LOSS_THREADS - 1) / (4 * LOSS_THREADS);
-    blocks = (int)std::max<long long>(1, std::min<long long>(want, num_sms()));
+    blocks = (int)std::max<long long>(1, std::min<long long>(want, 148));     // (the workspace's size must not depend on the device)
     per = (T + blocks - 1) / blocks;
     blocks = std::max(1, (T + per - 1) / std::max(per, 1));
 }
