@@ -137,11 +137,16 @@ struct Staging {
     uint8_t* buf;            // two buffers of STAGE_ROWS bytes
     int at;                  // the next one
     int lane;
+    bool whole = false;      // the last store read both
 
     // the next buffer, once the store that last used it has read it
     __device__ __forceinline__ uint8_t* acquire()
     {
-        if (lane == 0) bulk_wait_read<1>();
+        if (lane == 0) {
+            if (whole) bulk_wait_read<0>();
+            else bulk_wait_read<1>();
+        }
+        whole = false;
         __syncwarp();
         uint8_t* b = buf + at * STAGE_ROWS;
         at ^= 1;
@@ -153,6 +158,7 @@ struct Staging {
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
         at = 0;
+        whole = true;
         return buf;
     }
     __device__ __forceinline__ void store(const CUtensorMap* m, const uint8_t* b, int c0, int r0) const
@@ -210,7 +216,7 @@ __device__ __forceinline__ void epilogue32(const TcArgs& a, const CUtensorMap* t
         for (int i = 0; i < 32; ++i)
             if (cv && i < nr) z[i * e.ld_z] = __float2bfloat16_rn(v[i]);
     }
-    uint8_t* b = a.staged & (ST_OUT | ST_OUT32 | ST_RES) && e.out_f32 ? st.acquire_all() : a.staged & (ST_OUT | ST_RES) ? st.acquire() : nullptr;
+    uint8_t* b = a.staged & ST_OUT32 ? st.acquire_all() : a.staged & ST_OUT ? st.acquire() : nullptr;
     __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + st.lane;
     if ((a.staged & ST_RES) && e.out_f32) {
         const float* mine32 = reinterpret_cast<const float*>(b) + st.lane;
@@ -842,7 +848,8 @@ bool epilogue_maps(const TcProduct& p, int bn, const CUtensorMap& mA, int& stage
         if (!stored_map(mZ, e.z, p.C, p.R, e.ld_z, false)) return false;
     }
     const int piece = e.out_f32 ? 4 : 8;
-    if (e.residual && e.ld_r % piece == 0 && p.C % piece == 0) staged |= ST_RES;
+    // (only beside a staged output: each buffer that is taken is stored from, which acquire() counts on)
+    if (e.residual && (staged & (ST_OUT | ST_OUT32)) && e.ld_r % piece == 0 && p.C % piece == 0) staged |= ST_RES;
     return true;
 }
 

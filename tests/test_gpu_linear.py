@@ -77,16 +77,17 @@ def _close(name, got, want, bound):
                            f"{float(((got - want).abs() / (bound + 1e-37)).max()):.2f} of it")
 
 
-def _forward(M, N, K, dtype, act, out_f32=False, bias=True, residual=True, save=True, pad=0, seed=0):
+def _forward(M, N, K, dtype, act, out_f32=False, bias=True, residual=True, save=True, pad=0, seed=0, pads=None):
     g, dt = _gen(seed), DT[dtype]
+    y_pad, z_pad, r_pad = pads or (pad, pad, pad)
     out = torch.float32 if out_f32 else dt
     x, w = _mat(g, M, K, dt, pad=pad), _mat(g, N, K, dt, K ** -0.5, pad=pad)
     b = torch.randn(N, device="cuda", generator=g) if bias else None
-    r = _mat(g, M, N, out, pad=pad) if residual else None
+    r = _mat(g, M, N, out, pad=r_pad) if residual else None
     desc = moe.make_linear_desc(M, N, K, dtype, act, out_f32=out_f32, ld_w=K + pad)
     # poisoned, in rows of a wider buffer: what lies beside the rows must stay
-    ybuf = torch.full((M, N + pad), 777.0, device="cuda", dtype=out)
-    zbuf = torch.full((M, N + pad), 777.0, device="cuda", dtype=dt)
+    ybuf = torch.full((M, N + y_pad), 777.0, device="cuda", dtype=out)
+    zbuf = torch.full((M, N + z_pad), 777.0, device="cuda", dtype=dt)
     z = zbuf[:, :N] if save else None
     y = moe.Linear(desc, w, b).forward(x, residual=r, y=ybuf[:, :N], z=z)
     z64 = x.double() @ w.double().T + (b.double() if bias else 0)
@@ -97,8 +98,7 @@ def _forward(M, N, K, dtype, act, out_f32=False, bias=True, residual=True, save=
     _close("y", y, y64, ey + _round(out) * (y64.abs() + ey))
     if save:
         _close("z", z, z64, ez + _round(dt) * (z64.abs() + ez))
-    if pad:
-        assert (ybuf[:, N:] == 777.0).all() and (not save or (zbuf[:, N:] == 777.0).all())
+    assert (ybuf[:, N:] == 777.0).all() and (not save or (zbuf[:, N:] == 777.0).all())
 
 
 SIZES = [(1, 8, 8), (1, 1, 1), (1, 4096, 512), (2, 33, 17), (7, 129, 65), (16, 256, 1024), (17, 130, 200), (64, 256, 128),
@@ -127,9 +127,40 @@ def test_forward_row_strides(dtype, pad):
     _forward(300, 520, 333, dtype, "none", pad=pad)
 
 
+@pytest.mark.parametrize("pads", [(5, 0, 0), (0, 5, 0), (0, 0, 5), (5, 0, 5), (5, 5, 0), (0, 5, 5)])
+@pytest.mark.parametrize("out_f32", [False, True])
+def test_forward_row_strides_of_each_tensor(pads, out_f32):
+    """Each of y, z and the residual with rows that the wide path can and cannot address, beside the others."""
+    _forward(700, 1024, 256, "bf16", "silu", out_f32=out_f32, pads=pads)
+    _forward(64, 512, 256, "bf16", "none", out_f32=out_f32, pads=pads)
+
+
 def test_forward_large():
     _forward(4096, 2816, 1024, "bf16", "silu", save=False)
     _forward(5000, 3001, 1024, "bf16", "none", residual=False, save=False, out_f32=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(267, 6912, 1472), (700, 1024, 512), (128, 512, 256), (2000, 2048, 640)])
+def test_fp32_rows_beside_a_kept_pre_activation(M, N, K):
+    """The bf16 pre-activation and the fp32 result leave through the same buffers, several pieces in a row."""
+    for seed in range(3):
+        _forward(M, N, K, "bf16", "gelu", out_f32=True, bias=False, residual=seed == 1, seed=seed)
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 20, 4096), (300, 256, 14336), (16, 128, 8192), (2048, 130, 2048)])
+def test_fp32_results_of_long_sums(M, N, K):
+    """Without a rounding to bf16 a sum holds what fp32 can: the tensor cores' own accumulation (a rounding toward
+    zero, one step 2^-23, every 16 products) runs over at most 512 products, then fp32 additions take over, so the
+    error is at most (512 / 16 + K / 512 + 8) 2^-23 of the sum of the magnitudes (8: a cluster's partial sums)."""
+    g = _gen(K)
+    x, w = _mat(g, M, K, torch.bfloat16), _mat(g, N, K, torch.bfloat16, K ** -0.5)
+    bound = (32 + K / 512 + 8) * 2.0 ** -23
+    y = moe.Linear(moe.make_linear_desc(M, N, K, out_f32=True), w).forward(x)
+    _close("y", y, x.double() @ w.double().T, bound * (x.double().abs() @ w.double().abs().T))
+    xt, dy = x.t().contiguous(), _mat(g, K, N, torch.float32)               # a contraction over K rows
+    layer = moe.Linear(moe.make_linear_desc(K, N, M, out_f32=True, grad_f32=True), _mat(g, N, M, torch.bfloat16))
+    dw = layer.backward(xt, dy, need_dx=False)[1]
+    _close("dw", dw, dy.double().T @ xt.double(), (bound + 2.0 ** -23) * (dy.double().abs().T @ xt.double().abs()))
 
 
 @pytest.mark.parametrize("N", [8, 20, 64, 256])
