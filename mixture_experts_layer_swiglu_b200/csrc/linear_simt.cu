@@ -24,7 +24,16 @@ namespace moe {
 namespace {
 
 constexpr int LS_THREADS = 256;
-constexpr int LS_BK = 16;
+// Depth of a slice: 32 for the small tile, whose blocks are few per SM and wait for their loads.
+template <int TILE> constexpr int ls_bk() { return TILE == 64 ? 32 : 16; }
+template <int TILE> constexpr int ls_pieces() { return TILE * ls_bk<TILE>() / 4 / LS_THREADS; }    // of four, per thread
+
+// Row k of a 32-deep slice holds element i at i ^ skew<TILE>(k): groups of four change
+// places from one group of four rows to the next, so that the transposing stores
+// of a slice whose rows are contiguous along k meet no bank twice (16-deep ones
+// meet two at most, which costs less than the skew).
+template <int TILE>
+__host__ __device__ constexpr int skew(int k) { return TILE == 64 ? ((k >> 2) & 7) << 2 : 0; }
 
 // One operand's side of the tile: element (i, k) at i * rs + k * ks, one of them 1.
 struct Side {
@@ -34,17 +43,18 @@ struct Side {
     int vec;                 // 16-byte loads along the contiguous index are aligned
 };
 
-// A TILE x 16 slice into registers, in pieces of four along the contiguous
+// A slice of TILE elements x ls_bk into registers, in pieces of four along the contiguous
 // index; a piece that is cut by an edge (or not aligned) is loaded element by element.
 template <int TILE>
-__device__ __forceinline__ void fetch(const Side& s, int i0, int k0, int K, float4 (&v)[TILE / 64])
+__device__ __forceinline__ void fetch(const Side& s, int i0, int k0, int K, float4 (&v)[ls_pieces<TILE>()])
 {
+    constexpr int KQ = ls_bk<TILE>() / 4;
     const int t = threadIdx.x;
 #pragma unroll
-    for (int q = 0; q < TILE / 64; ++q) {
+    for (int q = 0; q < ls_pieces<TILE>(); ++q) {
         const int piece = t + q * LS_THREADS;
         const bool kc = s.ks == 1;
-        const int i = i0 + (kc ? piece / 4 : piece % (TILE / 4) * 4), k = k0 + (kc ? piece % 4 * 4 : piece / (TILE / 4));
+        const int i = i0 + (kc ? piece / KQ : piece % (TILE / 4) * 4), k = k0 + (kc ? piece % KQ * 4 : piece / (TILE / 4));
         const float* p = s.p + (long long)i * s.rs + (long long)k * s.ks;
         const int left = kc ? (i < s.n ? K - k : 0) : (k < K ? s.n - i : 0);
         if (s.vec && left >= 4) {
@@ -59,20 +69,22 @@ __device__ __forceinline__ void fetch(const Side& s, int i0, int k0, int K, floa
 }
 
 template <int TILE>
-__device__ __forceinline__ void stash(float (*d)[TILE + 4], const Side& s, const float4 (&v)[TILE / 64])
+__device__ __forceinline__ void stash(float (*d)[TILE + 4], const Side& s, const float4 (&v)[ls_pieces<TILE>()])
 {
+    constexpr int KQ = ls_bk<TILE>() / 4;
     const int t = threadIdx.x;
 #pragma unroll
-    for (int q = 0; q < TILE / 64; ++q) {
+    for (int q = 0; q < ls_pieces<TILE>(); ++q) {
         const int piece = t + q * LS_THREADS;
         if (s.ks == 1) {
-            const int i = piece / 4, k = piece % 4 * 4;
+            const int k = piece % KQ * 4, i = (piece / KQ) ^ skew<TILE>(k);
             d[k][i] = v[q].x;
             d[k + 1][i] = v[q].y;
             d[k + 2][i] = v[q].z;
             d[k + 3][i] = v[q].w;
         } else {
-            *reinterpret_cast<float4*>(&d[piece / (TILE / 4)][piece % (TILE / 4) * 4]) = v[q];
+            const int k = piece / (TILE / 4);
+            *reinterpret_cast<float4*>(&d[k][(piece % (TILE / 4) * 4) ^ skew<TILE>(k)]) = v[q];
         }
     }
 }
@@ -97,7 +109,7 @@ template <int TILE>
 __global__ void __launch_bounds__(LS_THREADS, TILE == 128 ? 2 : 4)
 linear_simt_kernel(const Side P, const Side Q, int K, const LinEpilogue epi, int splits, int tiles_c)
 {
-    constexpr int F = TILE / 16;                 // outputs per thread and direction
+    constexpr int F = TILE / 16, LS_BK = ls_bk<TILE>();      // outputs per thread and direction; depth
     extern __shared__ __align__(16) float s_dyn[];
     float(*sp)[LS_BK][TILE + 4] = reinterpret_cast<float(*)[LS_BK][TILE + 4]>(s_dyn);
     float(*sq)[LS_BK][TILE + 4] = sp + 2;
@@ -113,7 +125,7 @@ linear_simt_kernel(const Side P, const Side Q, int K, const LinEpilogue epi, int
         for (int j = 0; j < F / 2; ++j) acc2[i][j] = 0;
     pdl_wait();
     pdl_trigger();
-    float4 vp[TILE / 64], vq[TILE / 64];
+    float4 vp[ls_pieces<TILE>()], vq[ls_pieces<TILE>()];
     if (kb0 < kb1) {
         fetch<TILE>(P, r0, kb0 * LS_BK, K, vp);
         fetch<TILE>(Q, c0, kb0 * LS_BK, K, vq);
@@ -133,8 +145,8 @@ linear_simt_kernel(const Side P, const Side Q, int K, const LinEpilogue epi, int
             uint64_t b[F / 2];
 #pragma unroll
             for (int i = 0; i < F; i += 4) {
-                *reinterpret_cast<float4*>(a + i) = *reinterpret_cast<const float4*>(&sp[buf][k][ty * 4 + 16 * i]);
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sq[buf][k][tx * 4 + 16 * i]);
+                *reinterpret_cast<float4*>(a + i) = *reinterpret_cast<const float4*>(&sp[buf][k][(ty * 4 + 16 * i) ^ skew<TILE>(k)]);
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sq[buf][k][(tx * 4 + 16 * i) ^ skew<TILE>(k)]);
                 b[i / 2] = x.x;
                 b[i / 2 + 1] = x.y;
             }
@@ -185,7 +197,7 @@ moe_status launch(const SimtProduct& p, int splits, cudaStream_t st)
     const int tiles_c = cdiv(p.C, TILE);
     const long long tiles = (long long)cdiv(p.R, TILE) * tiles_c;
     if (tiles * splits >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
-    const int smem = std::max(4 * LS_BK * (TILE + 4) * 4, splits > 1 ? TILE * TILE * 4 : 0);
+    const int smem = std::max(4 * ls_bk<TILE>() * (TILE + 4) * 4, splits > 1 ? TILE * TILE * 4 : 0);
     auto* fn = linear_simt_kernel<TILE>;
     if (ensure_smem_attr(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return MOE_ERR_CUDA;
     auto side = [](const float* b, long long rs, long long ks, int n) {
@@ -197,23 +209,27 @@ moe_status launch(const SimtProduct& p, int splits, cudaStream_t st)
 
 }  // namespace
 
-// The tile and split of the smallest estimate, in us: a 16-deep step of a
-// 128 x 128 tile takes 1.3 alone on an SM and 2.5 beside another block, one of a
-// 64 x 64 tile 0.5 alone and 0.36 for each of up to four; 1.5 to add the tiles of a split.
+// The tile and split of the smallest estimate, in us, from measurements: a
+// 16-deep step of a 128 x 128 tile takes 1.5 alone on an SM and 2.9 beside
+// another block, a 32-deep step of a 64 x 64 tile 1.4, 2.4, 3.1 and 3.9 beside
+// none to three others; adding the tiles of a split 2.  Clusters of 4 and 8 fit on
+// 8/9 and 13/16 of the SMs.
 moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st)
 {
-    const int nkb = cdiv(p.K, LS_BK), sms = num_sms();
+    static const double small_step[4] = {1.4, 2.4, 3.1, 3.9};
+    const int sms = num_sms();
     int tile = 64, splits = 1;
     double least = 1e30;
     for (int t : {64, 128}) {
         const long long tiles = (long long)cdiv(p.R, t) * cdiv(p.C, t);
+        const int deep = t == 64 ? 32 : 16, most = t == 64 ? 4 : 2, steps = cdiv(p.K, deep);
         for (int S = 1; S <= 8; S *= 2) {
-            if (S > 1 && (t == 128 || nkb < 2 * S)) continue;
-            const long long blocks = tiles * S, room = (t == 128 ? 2 : 4) * (long long)sms;
-            const long long waves = (blocks + room - 1) / room;
-            const long long beside = std::min<long long>((blocks + sms - 1) / sms, t == 128 ? 2 : 4);
-            const double step = t == 128 ? (beside == 1 ? 1.3 : 2.5) : std::max(0.5, 0.36 * beside);
-            const double us = waves * (cdiv(nkb, S) * step + 1.0) + (S > 1 ? 1.5 : 0.0);
+            if (S > std::max(1, 2 * steps / 3)) continue;
+            const long long blocks = tiles * S, slots = S == 8 ? sms * 13 / 16 : S == 4 ? sms * 8 / 9 : sms;
+            const long long full = blocks / (slots * most), rest = blocks % (slots * most);
+            auto step = [&](long long beside) { return t == 64 ? small_step[beside - 1] : beside == 1 ? 1.5 : 2.9; };
+            const double waves = full * step(most) + (rest ? step((rest + slots - 1) / slots) : 0.0);
+            const double us = waves * cdiv(steps, S) + (S > 1 ? 2.0 : 0.0);
             if (us < least) { least = us; tile = t; splits = S; }
         }
     }
