@@ -210,10 +210,10 @@ moe_status launch(const SimtProduct& p, int splits, cudaStream_t st)
 }  // namespace
 
 // The tile and split of the smallest estimate, in us, from measurements: a
-// 16-deep step of a 128 x 128 tile takes 1.5 alone on an SM and 2.9 beside
+// 16-deep step of a 128 x 128 tile takes 1.9 alone on an SM and 2.9 beside
 // another block, a 32-deep step of a 64 x 64 tile 1.4, 2.4, 3.1 and 3.9 beside
-// none to three others; adding the tiles of a split 2.  Clusters of 4 and 8 fit on
-// 8/9 and 13/16 of the SMs.
+// none to three others; a tile's first loads and its stores 3 and 1.5; adding the
+// tiles of a split 8 and 1.  Clusters of 4 and 8 fit on 8/9 and 13/16 of the SMs.
 moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st)
 {
     static const double small_step[4] = {1.4, 2.4, 3.1, 3.9};
@@ -224,12 +224,12 @@ moe_status launch_linear_simt(const SimtProduct& p, cudaStream_t st)
         const long long tiles = (long long)cdiv(p.R, t) * cdiv(p.C, t);
         const int deep = t == 64 ? 32 : 16, most = t == 64 ? 4 : 2, steps = cdiv(p.K, deep);
         for (int S = 1; S <= 8; S *= 2) {
-            if (S > std::max(1, 2 * steps / 3)) continue;
+            if (S > 2 * steps) continue;
             const long long blocks = tiles * S, slots = S == 8 ? sms * 13 / 16 : S == 4 ? sms * 8 / 9 : sms;
             const long long full = blocks / (slots * most), rest = blocks % (slots * most);
-            auto step = [&](long long beside) { return t == 64 ? small_step[beside - 1] : beside == 1 ? 1.5 : 2.9; };
+            auto step = [&](long long beside) { return t == 64 ? small_step[beside - 1] : beside == 1 ? 1.9 : 2.9; };
             const double waves = full * step(most) + (rest ? step((rest + slots - 1) / slots) : 0.0);
-            const double us = waves * cdiv(steps, S) + (S > 1 ? 2.0 : 0.0);
+            const double us = waves * cdiv(steps, S) + (full + (rest > 0)) * (t == 64 ? 1.5 : 3.0) + (S > 1 ? (t == 64 ? 1.0 : 8.0) : 0.0);
             if (us < least) { least = us; tile = t; splits = S; }
         }
     }
