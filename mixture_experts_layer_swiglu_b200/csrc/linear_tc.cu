@@ -895,7 +895,7 @@ bool promoted(const TcProduct& p, int splits) { return p.epi.out_f32 && cdiv(cdi
 //          two, and at least a loaded memory latency over the stages in flight;
 //          at least the loads of all tiles at 13 TB/s, the most that L2 gave;
 //          the rest 4.6 + 0.0065 bn, and 1 + 0.02 bn to add partial tiles;
-//   fp32 results that change accumulators: 0.07 a step (pair), 0.5 a change (split).
+//   fp32 results that change accumulators: 0.07 a step (pair), 0.8 a change (split).
 Plan choose(const TcProduct& p)
 {
     const int nkb = cdiv(p.K, KB), sms = num_sms();
@@ -925,7 +925,7 @@ Plan choose(const TcProduct& p)
             const int n = p.b_parts == 3 ? 64 * sp_boxes(p) : bn;
             const double step = std::max(occ == 2 ? 0.15 + 0.0024 * n : 0.18 + 0.0004 * n, 1.5 / stages);
             const double loads = (double)tiles * nkb * sp_stage_bytes(p, bn) / 13e6;
-            const double sums = promoted(p, S) ? 0.5 * cdiv(cdiv(nkb, S), PROMOTE_STEPS) : 0.0;
+            const double sums = promoted(p, S) ? 0.8 * cdiv(cdiv(nkb, S), PROMOTE_STEPS) : 0.0;
             const double t = std::max(waves * (cdiv(nkb, S) * step + sums + 0.5 + 0.0065 * bn), loads) + 4.1 +
                              (S > 1 ? 1.0 + 0.02 * bn : 0.0);
             if (t < least) { least = t; best = Plan{0, bn, S, stages, occ, 1}; }
