@@ -139,6 +139,13 @@ struct Staging {
     int lane;
     bool whole = false;      // the last store read both
 
+    // the one buffer of a light epilogue
+    __device__ __forceinline__ uint8_t* acquire_one()
+    {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        return buf;
+    }
     // the next buffer, once the store that last used it has read it
     __device__ __forceinline__ uint8_t* acquire()
     {
@@ -310,11 +317,24 @@ __device__ __forceinline__ void acc_add(uint32_t t, int j, int part, bool first,
     for (int i = 0; i < 32; ++i) sum[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
 }
 
+// The epilogue of a product that is only rounded to bf16 (bias apart): one
+// buffer of STAGE_ROWS bytes per warp, few registers.
+__device__ __forceinline__ void light_epilogue32(const CUtensorMap* tmOut, const uint32_t (&acc)[32], long long r0, int c0,
+                                                 float bias, Staging& st)
+{
+    uint8_t* b = st.acquire_one();
+    __nv_bfloat16* mine = reinterpret_cast<__nv_bfloat16*>(b) + st.lane;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) mine[i * BOX_C] = __float2bfloat16_rn(__uint_as_float(acc[i]) + bias);
+    st.store(tmOut, b, c0, (int)r0);
+}
+
 // ------------------------------------------------------------ pair form
 constexpr int PR_MAX_STAGES = 10;
-constexpr int PR_EPI_WARPS = 8;                                // two per TMEM lane quarter, alternate 32-row chunks
-constexpr int PR_THREADS = 64 + 32 * PR_EPI_WARPS;
-constexpr int PR_STAGING = PR_EPI_WARPS * 2 * STAGE_ROWS;
+// Epilogue warps: two per TMEM lane quarter, alternate 32-row chunks, or four.
+template <bool LIGHT> constexpr int pr_epi_warps() { return LIGHT ? 16 : 8; }
+template <bool LIGHT> constexpr int pr_threads() { return 64 + 32 * pr_epi_warps<LIGHT>(); }
+constexpr int PR_STAGING = 16 * STAGE_ROWS;
 constexpr int PR_SMEM = 227 * 1024;
 // as many stages as fit: 6 of 32 KB (bn = 256) to 9 of 20 KB (bn = 64)
 __host__ __device__ constexpr int pr_stages(int b_bytes)
@@ -334,8 +354,8 @@ __device__ __forceinline__ void tile_at(const TcArgs& a, int tile, int& tr, int&
     tr = band * a.group_r + in - tc * h;
 }
 
-template <bool AMN, bool BMN, int ACT, bool PROMOTE>
-__global__ void __launch_bounds__(PR_THREADS, 1)
+template <bool AMN, bool BMN, int ACT, bool PROMOTE, bool LIGHT>
+__global__ void __launch_bounds__(pr_threads<LIGHT>(), 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
                    const __grid_constant__ TcArgs a)
@@ -364,7 +384,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         // full, empty, acc_full, acc_empty and mma_done lie in a row: a barrier per lane
         static_assert(2 * PR_MAX_STAGES + 5 <= 31, "");
         const int first = 2 * PR_MAX_STAGES + 2;
-        if (lane < 2 * PR_MAX_STAGES + 5) mbar_init(full + lane, lane == first || lane == first + 1 ? 2 * PR_EPI_WARPS : 1);
+        if (lane < 2 * PR_MAX_STAGES + 5) mbar_init(full + lane, lane == first || lane == first + 1 ? 2 * pr_epi_warps<LIGHT>() : 1);
         if (lane == 31) *abort_flag = 0;
         fence_barrier_init();
     }
@@ -456,8 +476,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             mbar_wait(mma_done, 0);
         }
     } else {
+        constexpr int STEP = 32 * (pr_epi_warps<LIGHT>() / 4);          // rows between a warp's chunks
         const int q = warp & 3, half = (warp - 2) >> 2;
-        Staging st{staging + (warp - 2) * 2 * STAGE_ROWS, 0, lane};
+        Staging st{staging + (warp - 2) * (LIGHT ? 1 : 2) * STAGE_ROWS, 0, lane};
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = cluster; tile < total; tile += n_clusters) {
@@ -468,7 +489,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             const int rows = (int)min((long long)a.bn, a.R - r0);
             const float bias = a.epi.bias && c0 + lane < a.C ? a.epi.bias[c0 + lane] : 0.f;
             uint4 res[8] = {};
-            if (!PROMOTE && (a.staged & ST_RES)) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, lane);
+            if (!PROMOTE && !LIGHT && (a.staged & ST_RES)) residual_load(a, res, r0 + half * 32, rows - half * 32, c0, lane);
             const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16);
             if constexpr (PROMOTE) {
                 uint32_t sum0[32], sum1[32];                   // of this warp's two chunks of rows (bn <= 128)
@@ -493,11 +514,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             } else {
                 if (!warp_wait(&acc_full[acc], aph)) { *abort_flag = 1; break; }
                 tc_fence_after();
-                for (int j = half * 32; j < rows; j += 64) {
+                for (int j = half * 32; j < rows; j += STEP) {
                     uint32_t v[32];
                     tmem_ld32(t0 + acc * 256 + j, v);
                     tc_wait_ld_regs(v);
-                    if (c0 < a.C) epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 64, c0, bias, st);
+                    if (c0 >= a.C) continue;
+                    if constexpr (LIGHT) light_epilogue32(&tmOut, v, r0 + j, c0, bias, st);
+                    else epilogue32<ACT>(a, &tmOut, &tmZ, v, res, r0 + j, rows - j, 64, c0, bias, st);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -958,11 +981,20 @@ moe_status launch_pair(const TcProduct& p, const Plan& pl, cudaStream_t st)
     if (!epilogue_maps(p, pl.bn, mA, a.staged, &mO, &mZ)) return MOE_ERR_CUDA;
     a.stages = pr_stages((int)a.b_bytes);
     a.chunk = PROMOTE_STEPS;
-    auto* fn = linear_pair_kernel<AMN, BMN, ACT, PROMOTE>;
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), PR_SMEM);
-    if (e != cudaSuccess) return cuda_status(e);
     const int clusters = (int)std::min<long long>(tiles, num_sms() / 2);
-    return launch_dependent(fn, dim3(2 * clusters), PR_THREADS, PR_SMEM, 2, st, mA, mB, mO, mZ, a);
+    auto go = [&](auto* fn, int threads) {
+        const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), PR_SMEM);
+        if (e != cudaSuccess) return cuda_status(e);
+        return launch_dependent(fn, dim3(2 * clusters), threads, PR_SMEM, 2, st, mA, mB, mO, mZ, a);
+    };
+    // Sixteen epilogue warps where a tile's MMAs (up to 512 of the contraction) are
+    // shorter than its epilogue: 16384 x 2048 x 20 29.0 -> 24.8 us, 8192 x 14336 x
+    // 512 114 -> 108; with longer tiles eight are as fast or faster (K = 1024: 9.8
+    // against 10.3).
+    if constexpr (ACT == MOE_ACT_NONE && !PROMOTE)
+        if (a.nkb * KB <= 512 && a.staged == ST_OUT && !p.epi.residual && !p.epi.z)
+            return go(linear_pair_kernel<AMN, BMN, ACT, PROMOTE, true>, pr_threads<true>());
+    return go(linear_pair_kernel<AMN, BMN, ACT, PROMOTE, false>, pr_threads<false>());
 }
 
 template <bool AMN, bool BMN, int ACT, int PARTS, bool PROMOTE>
