@@ -396,16 +396,17 @@ __global__ void __launch_bounds__(RB_THREADS, 4) route_backward_kernel(const Rou
         float z[N][EPL], d[N][EPL];
         int e[N];
         float g[N], dg[N];
-        bool live[N];
+        bool live[N], on[N];                    // on: the losses count the token
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             live[u] = base + grp + u * stride < a.T;
+            on[u] = nin[u];
             e[u] = ne[u];
             g[u] = ng[u];
             dg[u] = ndg[u];
             if (a.dgate && live[u] && l < a.k && (e[u] < 0 || e[u] >= a.E)) { set_status(MOE_ERR_DEVICE_BOUNDS); e[u] = -1; }
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) z[u][i] = nin[u] ? nz[u][i] : -INFINITY;
+            for (int i = 0; i < EPL; ++i) z[u][i] = on[u] ? nz[u][i] : -INFINITY;
         }
         fetch(base + stride * N);
         if (a.dgate) {
@@ -457,7 +458,8 @@ __global__ void __launch_bounds__(RB_THREADS, 4) route_backward_kernel(const Rou
 #pragma unroll
             for (int u = 0; u < N; ++u)
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) d[u][i] = z[u][i] * (c_bal * (wf[i] - dot[u]) + c_z * lse[u]);
+                for (int i = 0; i < EPL; ++i)      // (0 for a token that is not counted, also where dlosses is not finite)
+                    d[u][i] = on[u] ? z[u][i] * (c_bal * (wf[i] - dot[u]) + c_z * lse[u]) : 0.f;
         } else {
 #pragma unroll
             for (int u = 0; u < N; ++u)

@@ -324,6 +324,31 @@ def test_no_rows(dtype):
     assert dx.shape == (0, 64) and not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_object_on_two_streams_at_once(dtype):
+    """Calls of one Linear that overlap share its weights only (odd strides: each has a workspace of its own)."""
+    g = _gen(5)
+    M, N, K = 201, 333, 517
+    w = _mat(g, N, K, DT[dtype], 0.05)
+    layer = moe.Linear(moe.make_linear_desc(M=M, N=N, K=K, dtype=dtype, act="silu"), w,
+                       torch.randn(N, device="cuda", generator=g))
+    xs = [_mat(g, M + 7 * i, K, DT[dtype]) for i in range(2)]
+    dys = [_mat(g, M + 7 * i, N, DT[dtype]) for i in range(2)]
+    zs = [torch.empty((M + 7 * i, N), dtype=DT[dtype], device="cuda") for i in range(2)]
+    want = [(layer.forward(x, z=z), *layer.backward(x, dy, z=z)) for x, dy, z in zip(xs, dys, zs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for n in range(8):
+        for i in range(2):
+            st = streams[i] if n % 2 else streams[i].cuda_stream            # an object or a handle
+            got[i].append((layer.forward(xs[i], stream=st), *layer.backward(xs[i], dys[i], z=zs[i], stream=st)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(run, want[i]))
+
+
 def test_side_stream_and_graph_replay():
     g = _gen(12)
     x, w, z = _mat(g, 129, 264, torch.bfloat16), _mat(g, 250, 264, torch.bfloat16, 0.1), None

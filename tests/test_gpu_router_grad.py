@@ -130,6 +130,24 @@ def test_padded_batches_and_expert_weights(T, E, k):
     _check_loss(z, idx, gate, dgate, k, mask.bool(), None)
 
 
+@pytest.mark.parametrize("E,k", [(8, 2), (20, 2), (128, 4), (200, 8)])
+def test_gradient_of_uncounted_tokens_beside_an_overflowed_loss_scale(E, k):
+    """A token that the losses leave out has no gradient from them, whatever their own gradients are."""
+    T = 70
+    z, idx, gate, dgate = _routed(T, E, k)
+    mask = (torch.arange(T, device="cuda") % 3 != 0).to(torch.uint8)
+    desc = _desc(T, E, k)
+    b = moe.RouterGradBuffers(desc)
+    moe.moe_balance_loss(desc, z, idx, mask, None, b.counts, b.prob_mean, b.losses, b.workspace)
+    dl = torch.tensor([float("inf"), float("nan")], device="cuda")
+    moe.moe_route_backward(desc, z, idx, gate, None, mask, None, b.counts, dl, b.dlogits)
+    assert not b.dlogits[::3].any() and b.dlogits[1::3].isnan().all()
+    moe.moe_route_backward(desc, z, idx, gate, dgate, mask, None, b.counts, dl, b.dlogits)
+    want = torch.empty_like(z)
+    moe.moe_route_backward(desc, z, idx, gate, dgate, None, None, None, None, want)
+    assert torch.equal(b.dlogits[::3], want[::3])
+
+
 def test_no_counted_token_and_no_token():
     z, idx, gate, dgate = _routed(40, 8, 2)
     b = _check_loss(z, idx, gate, dgate, 2, torch.zeros(40, dtype=torch.uint8, device="cuda"))
