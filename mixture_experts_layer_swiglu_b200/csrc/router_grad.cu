@@ -42,6 +42,7 @@ struct LossArgs {
     int32_t* part_c;      // [blocks, E + 1] slot counts and counted tokens
     float* part_z;        // [blocks] sums of lse^2
     int T, E, k, blocks, tokens_per_block;
+    double scale;         // E / k
 };
 
 constexpr int LOSS_THREADS = 1024;
@@ -87,10 +88,15 @@ __device__ __forceinline__ void softmax_rows(float (&z)[N][EPL], float (&lse)[N]
         for (int i = 1; i < EPL; ++i) m[t] = fmaxf(m[t], z[t][i]);
     }
     // (fmaxf drops a NaN; it comes back through exp and the sum)
+    if constexpr (L == 32) {               // one instruction for five shuffles (65,536 x 256, both directions: 52.9 -> 52.3 us)
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1)
+        for (int t = 0; t < N; ++t) asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(m[t]));
+    } else {
 #pragma unroll
-        for (int t = 0; t < N; ++t) m[t] = fmaxf(m[t], __shfl_xor_sync(FULL, m[t], o));
+        for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int t = 0; t < N; ++t) m[t] = fmaxf(m[t], __shfl_xor_sync(FULL, m[t], o));
+    }
 #pragma unroll
     for (int t = 0; t < N; ++t) {
         // exp(z - m) with the row's maximum; a row of -inf only: exp(-inf - 0) = 0
@@ -117,18 +123,18 @@ __device__ __forceinline__ void softmax_rows(float (&z)[N][EPL], float (&lse)[N]
 }
 
 // The totals -> the outputs, by one block: sp [E] probability sums, sc [E + 1] counts, z the lse^2 sum.
-__device__ void loss_finish(const LossArgs& a, const float* sp, const int32_t* sc, double zsum)
+__device__ void loss_finish(const LossArgs& a, const float* sp, const int32_t* sc, const float* sw, double zsum)
 {
     __shared__ double s_red[LOSS_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = sc[a.E];
-    const double inv = n > 0 ? 1.0 / n : 0.0;
+    const double inv = n > 0 ? 1.0f / (float)n : 0.f;
     double v = 0.0;
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         const double pm = sp[e] * inv;
         a.prob_mean[e] = (float)pm;
         a.counts[e] = sc[e];
-        v += pm * (a.weight ? sc[e] * (double)a.weight[e] : (double)sc[e]);
+        v += pm * (sc[e] * (double)sw[e]);
     }
     if (threadIdx.x == 0) a.counts[a.E] = n;
 #pragma unroll
@@ -140,7 +146,7 @@ __device__ void loss_finish(const LossArgs& a, const float* sp, const int32_t* s
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     if (lane == 0) {
-        a.losses[0] = (float)(v * inv * a.E / a.k);
+        a.losses[0] = (float)(v * inv * a.scale);
         a.losses[1] = (float)(zsum * inv);
     }
 }
@@ -156,6 +162,7 @@ __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossAr
 {
     __shared__ float s_p[LOSS_WARPS][kMaxE];
     __shared__ int32_t s_c[kMaxE + 1];
+    __shared__ float s_w[kMaxE];
     __shared__ float s_z[LOSS_WARPS];
     constexpr int G = 32 / L;                       // tokens side by side in a warp
     constexpr int N = 2;                            // and one after another
@@ -167,6 +174,8 @@ __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossAr
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    if (a.blocks == 1)
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_w[e] = a.weight ? a.weight[e] : 1.f;
     float acc[EPL], zacc = 0.f;
     int live_n = 0;
 #pragma unroll
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossAr
     for (int w = 0; w < warps; ++w) zs += s_z[w];
     if (alone) {
         __syncthreads();
-        loss_finish(a, s_p[0], s_c, zs);
+        loss_finish(a, s_p[0], s_c, s_w, zs);
         return;
     }
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.part_c[(long long)blockIdx.x * (a.E + 1) + e] = s_c[e];
@@ -248,29 +257,35 @@ __global__ void __launch_bounds__(LOSS_THREADS) balance_loss_kernel(const LossAr
 
 // The blocks' sums: one cluster, each of its blocks a range of them (all loads
 // of a warp's rows at once), then their sums in order of rank.  (One block alone
-// took 38 us for 296 x 256 sums.)
+// took 38 us for 296 x 256 sums.)  Bound by the latencies of one load, the
+// cluster's barriers and the last sums: 4.4 us after the pass (of 8.0 for 16,383 x
+// 20, 21.2 for 65,536 x 256).  Half the warps where a row of sums needs few loads:
+// 16,383 x 20 8.0 against 8.5 us; with 256 columns 21.7 against 21.2.
 __global__ void __launch_bounds__(LOSS_THREADS)
 balance_loss_finish_kernel(const LossArgs a)
 {
     __shared__ float s_p[LOSS_WARPS][kMaxE];
+    __shared__ float s_w[kMaxE];
     __shared__ float s_sum[kMaxE];
     __shared__ int32_t s_c[kMaxE + 1];
     __shared__ int32_t s_cnt[kMaxE + 1];
     __shared__ double s_z;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
     const int b0 = (int)((long long)a.blocks * rank / LOSS_CLUSTER), b1 = (int)((long long)a.blocks * (rank + 1) / LOSS_CLUSTER);
-    for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) s_c[e] = 0;
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) s_c[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    if (rank == 0)
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) s_w[e] = a.weight ? a.weight[e] : 1.f;
     float p[kMaxE / 32];
     int c[kMaxE / 32 + 1];
 #pragma unroll
     for (int i = 0; i < kMaxE / 32; ++i) { p[i] = 0.f; c[i] = 0; }
     c[kMaxE / 32] = 0;
-    for (int b = b0 + warp; b < b1; b += LOSS_WARPS) {
+    for (int b = b0 + warp; b < b1; b += warps) {
 #pragma unroll
         for (int i = 0; i < kMaxE / 32; ++i)
             if (lane + 32 * i < a.E) p[i] += a.part_p[(long long)b * a.E + lane + 32 * i];
@@ -292,15 +307,15 @@ balance_loss_finish_kernel(const LossArgs a)
         if (lane == 0) s_z = z;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += LOSS_THREADS) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float v = 0.f;
-        for (int w = 0; w < LOSS_WARPS; ++w) v += s_p[w][e];
+        for (int w = 0; w < warps; ++w) v += s_p[w][e];
         s_sum[e] = v;
     }
     cl.sync();
     if (rank == 0) {
         double zs = 0.0;
-        for (int e = threadIdx.x; e <= a.E; e += LOSS_THREADS) {
+        for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
             float v = 0.f;
             int n = 0;
 #pragma unroll
@@ -314,7 +329,7 @@ balance_loss_finish_kernel(const LossArgs a)
         if (threadIdx.x == 0)
             for (int r = 0; r < LOSS_CLUSTER; ++r) zs += *cl.map_shared_rank(&s_z, r);
         __syncthreads();
-        loss_finish(a, s_p[0], s_cnt, zs);
+        loss_finish(a, s_p[0], s_cnt, s_w, zs);
     }
     cl.sync();
 }
@@ -928,6 +943,7 @@ moe_status moe_balance_loss(const moe_layer_desc* d, const float* logits, const 
     a.T = d->T;
     a.E = router_rows(d);
     a.k = d->top_k;
+    a.scale = (double)a.E / a.k;
     int threads;
     loss_blocks(a.T, a.E, a.blocks, a.tokens_per_block, threads);
     char* p = static_cast<char*>(workspace);
@@ -942,7 +958,8 @@ moe_status moe_balance_loss(const moe_layer_desc* d, const float* logits, const 
     MOE_LANES(a.E, CALL);
 #undef CALL
     if (r != MOE_OK || a.blocks == 1) return r;
-    return launch_dependent(balance_loss_finish_kernel, dim3(LOSS_CLUSTER), LOSS_THREADS, 0, LOSS_CLUSTER, st, a);
+    return launch_dependent(balance_loss_finish_kernel, dim3(LOSS_CLUSTER), a.E <= 128 ? LOSS_THREADS / 2 : LOSS_THREADS, 0,
+                            LOSS_CLUSTER, st, a);
 }
 
 moe_status moe_route_backward(const moe_layer_desc* d, const float* logits, const int32_t* topk_idx,
