@@ -324,6 +324,22 @@ def test_no_rows(dtype):
     assert dx.shape == (0, 64) and not dw.any() and not db.any()
 
 
+def test_strided_vectors_and_host_weights_are_refused():
+    w = torch.ones((32, 64), device="cuda", dtype=torch.bfloat16)
+    x, dy = torch.ones((9, 64), device="cuda", dtype=torch.bfloat16), torch.ones((9, 32), device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        moe.Linear(moe.make_linear_desc(9, 32, 64), w, torch.ones(64, device="cuda")[::2])
+    layer = moe.Linear(moe.make_linear_desc(9, 32, 64), w, torch.ones(32, device="cuda"))
+    with pytest.raises(ValueError):
+        layer.backward(x, dy, db=torch.ones(64, device="cuda")[::2])
+    with pytest.raises(ValueError):
+        layer.backward(x, dy, dw=torch.ones((32, 72), device="cuda", dtype=torch.bfloat16)[:, :64])
+    layer.w = w.cpu()                                  # exchanged for a tensor that the library cannot read
+    for call in (lambda: layer.forward(x), lambda: layer.backward(x, dy)):
+        with pytest.raises(ValueError):
+            call()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_object_on_two_streams_at_once(dtype):
     """Calls of one Linear that overlap share its weights only (odd strides: each has a workspace of its own)."""
